@@ -89,7 +89,8 @@ typedef enum {
 typedef enum { JT_DTYPE_F32 = 0, JT_DTYPE_BF16 = 1 } jt_dtype;
 typedef enum { JT_RULE_GREEDY = 0, JT_RULE_MARGIN = 1 } jt_rule;
 typedef enum { JT_OP_TREE_BUILD = 0, JT_OP_TREE_ATTN = 1, JT_OP_VERIFY_ACCEPT = 2,
-               JT_OP_TREE_TOPW = 3, JT_OP_TREE_BUILD_MIXED = 4, JT_OP_TREE_POLICY = 5 } jt_op;
+               JT_OP_TREE_TOPW = 3, JT_OP_TREE_BUILD_MIXED = 4, JT_OP_TREE_POLICY = 5,
+               JT_OP_CHUNK_ATTN = 6, JT_OP_KV_COMMIT = 7, JT_OP_QKV_APPEND = 8 } jt_op;
 
 /* Limits of this build. */
 #define JT_MAX_TREE 256   /* B_b (bitset width) */
@@ -108,6 +109,10 @@ typedef enum { JT_OP_TREE_BUILD = 0, JT_OP_TREE_ATTN = 1, JT_OP_VERIFY_ACCEPT = 
  *   TREE_TOPW:     nseq*N rows given as nseq (N=1), W, V
  *   TREE_ATTN:     nseq, total_nodes, Hq, Hkv, D, max_pages, max_tree
  *   VERIFY_ACCEPT: nseq, total_nodes
+ *   CHUNK_ATTN:    nseq, total_nodes (tokens), Hq, Hkv, D, max_pages,
+ *                  max_tree (the longest chunk); enough for either dtype
+ *   KV_COMMIT:     nseq
+ *   QKV_APPEND:    (256 bytes: the header only)
  */
 size_t jt_workspace_size(int op, int nseq, int N, int W, int64_t V, int total_nodes,
                          int Hq, int Hkv, int D, int max_pages, int max_tree);
@@ -411,6 +416,112 @@ jt_status jt_verify_accept_stochastic(const float* target_logits, const float* d
                                       int total_nodes, const double* u_accept, const double* u_bonus,
                                       int32_t* accept_len, int32_t* path, int32_t* bonus, void* ws,
                                       size_t ws_bytes, jt_stream_t stream);
+
+/*
+ * jt_qkv_append -- new tokens' queries, keys and values from the packed
+ * projection: per-head RMS norm of q and k, position rotation, and the write
+ * of k and v into the paged cache, in one pass.  (The pages leave the cache's
+ * contents to the serving system; this is the step before either attention.)
+ *   qkv:      [total_nodes, row_stride] (dtype), row i = the heads of token i:
+ *             Hq query heads, Hkv key heads, Hkv value heads of D elements;
+ *             row_stride (elements) >= (Hq + 2 Hkv) * D.  Hq = 0: keys and
+ *             values only (q_out may be NULL).
+ *   q_weight, k_weight: [D] (dtype) or NULL (no norm of those heads):
+ *             y = x * rsqrt(mean(x^2) + eps) * weight.
+ *   cos_sin:  fp32 [max_pos, rot_dim], row = position: rot_dim/2 cosines, then
+ *             rot_dim/2 sines of the position's angles.  rot_dim = 0: no
+ *             rotation (cos_sin may be NULL).  rot_dim <= D is a multiple of
+ *             16 (bf16) or 8 (fp32); elements from rot_dim on are not rotated.
+ *   interleaved: 0: pair j is elements (j, j + rot_dim/2); 1: (2j, 2j + 1).
+ *             (a, b) -> (a cos_j - b sin_j, b cos_j + a sin_j).
+ *   depth:    int32 [total_nodes] or NULL.  Token i of sequence b (global
+ *             index tree_off[b] + i) has position L_b + depth, as a tree's
+ *             nodes have, or L_b + i with NULL (new tokens in order); its k and
+ *             v go to logical slot L_b + i either way.
+ *   dtype, block_table, max_pages, num_pages, prefix_len, tree_off,
+ *   page_size, k_cache, v_cache: as in jt_tree_attn_paged; D in {64, 128}
+ *             (bf16) or {32, 64, 96, 128} (fp32).  A sequence may have any
+ *             number of new tokens, none included (tree_off[b+1] ==
+ *             tree_off[b]).
+ *   q_out:    [total_nodes, Hq, D] (dtype).
+ * Everything is computed in fp32 and rounded once; without norm and rotation
+ * the bits are copied.  A token whose sequence has contents out of range,
+ * whose page is outside the pool or whose position is not below max_pos is
+ * skipped (nothing of it is written) and raises JT_ERR_INVALID (device-side).
+ * total_nodes = 0 does nothing.  qkv, weights, cos_sin, q_out and the caches
+ * are 16-byte aligned (row_stride included) and do not overlap.
+ * Workspace: 256 bytes.
+ */
+jt_status jt_qkv_append(const void* qkv, int dtype, int64_t row_stride, const void* q_weight,
+                        const void* k_weight, float eps, const float* cos_sin, int max_pos,
+                        int rot_dim, int interleaved, const int32_t* depth,
+                        const int32_t* block_table, int max_pages, int num_pages,
+                        const int32_t* prefix_len, const int32_t* tree_off, int nseq,
+                        int total_nodes, int Hq, int Hkv, int D, int page_size, void* q_out,
+                        void* k_cache, void* v_cache, void* ws, size_t ws_bytes,
+                        jt_stream_t stream);
+
+/*
+ * jt_chunk_attn_paged -- causal attention of new tokens over a paged KV cache:
+ * prompts in chunks of any length, single tokens, or a ragged mix of both in
+ * one call (the forward that fills the prefix the tree step reads).
+ *   q:        [total_tokens, Hq, D] (dtype), the new tokens' queries.
+ *   chunk_off: int32 [nseq+1]: sequence b owns tokens chunk_off[b] ..
+ *             chunk_off[b+1]-1, B_b of them, 0 <= B_b <= max_chunk; rows at or
+ *             beyond chunk_off[nseq] are neither read nor written.
+ *   prefix_len: int32 [nseq], L_b tokens cached before; the new tokens' K/V are
+ *             in the slots L_b .. L_b + B_b - 1 (jt_qkv_append puts them
+ *             there); L_b + B_b <= max_pages * page_size.
+ * Token i of sequence b, query head h (KV head h / (Hq/Hkv)) attends to slots
+ * 0 .. L_b + i; what lies in other slots, infinities and NaN included, has no
+ * effect on it.
+ *   k_cache, v_cache, block_table, max_pages, num_pages, page_size, scale,
+ *   dtype: as in jt_tree_attn_paged.  bf16: D in {64, 128}, Hq/Hkv <= 128;
+ *             fp32: D in {32, 64, 96, 128}, Hq/Hkv <= 64; else
+ *             JT_ERR_UNSUPPORTED.
+ *   out:      [total_tokens, Hq, D] (dtype), lse: fp32 [total_tokens, Hq] or
+ *             NULL, as in jt_tree_attn_paged.
+ * The bf16 path runs on CTA pairs with the key tiles of all (sequence, KV
+ * head, query-tile pair) units cut into equal ranges, planned on the device;
+ * repeated calls give identical bits.  total_tokens = 0 does nothing.
+ * Workspace: jt_workspace_size(JT_OP_CHUNK_ATTN, nseq, 0, 0, 0, total_tokens,
+ * Hq, Hkv, D, max_pages, max_chunk), sized for the current device; its first
+ * 4096 bytes must be zero before its first use, and stay valid from call to
+ * call.  A workspace of this operator serves calls of this operator only.
+ */
+jt_status jt_chunk_attn_paged(const void* q, const void* k_cache, const void* v_cache, int dtype,
+                              const int32_t* block_table, int max_pages, int num_pages,
+                              const int32_t* prefix_len, const int32_t* chunk_off, int nseq,
+                              int total_tokens, int max_chunk, int Hq, int Hkv, int D,
+                              int page_size, float scale, void* out, float* lse, void* ws,
+                              size_t ws_bytes, jt_stream_t stream);
+
+/*
+ * jt_kv_commit -- after the acceptance, the accepted path becomes part of the
+ * prefix: for d = 1 .. accept_len[b] the K/V of the path's node at depth d
+ * move from logical slot L_b + path[b][d] to slot L_b + d, in every layer, and
+ * new_prefix[b] = L_b + accept_len[b] + 1 (the root and the accepted nodes;
+ * the bonus token is the next step's root).
+ *   k_cache, v_cache: `layers` caches [num_pages, page_size, Hkv, D] (dtype),
+ *             layer_stride elements apart (one layer: any value); the block
+ *             table serves all layers.  Hkv * D * element size is a multiple
+ *             of 16, else JT_ERR_UNSUPPORTED.
+ *   accept_len, path (int32 [nseq], [nseq, N+1]): jt_verify_accept*'s outputs.
+ *   prefix_len, tree_off, block_table: as in jt_tree_attn_paged.
+ *   new_prefix: int32 [nseq]; may be prefix_len itself (updated in place).
+ * A sequence whose accept_len, path (strictly rising from node 0), lengths or
+ * pages are out of range keeps its cache, its new_prefix entry is left as it
+ * was, and JT_ERR_INVALID is raised (device-side).  Pages that hold slots L_b ..
+ * L_b + B_b - 1 belong to one sequence alone.
+ * Workspace: jt_workspace_size(JT_OP_KV_COMMIT, nseq, ...); 256 bytes suffice
+ * when new_prefix and prefix_len do not overlap.
+ */
+jt_status jt_kv_commit(void* k_cache, void* v_cache, int dtype, int layers, int64_t layer_stride,
+                       const int32_t* block_table, int max_pages, int num_pages,
+                       const int32_t* prefix_len, const int32_t* tree_off,
+                       const int32_t* accept_len, const int32_t* path, int nseq, int N, int Hkv,
+                       int D, int page_size, int32_t* new_prefix, void* ws, size_t ws_bytes,
+                       jt_stream_t stream);
 
 /*
  * jt_check -- synchronise `stream`, read the device-side error flag of a

@@ -1,0 +1,119 @@
+"""Host-side checks of jt_qkv_append, jt_chunk_attn_paged and jt_kv_commit: what
+they refuse, before anything is enqueued (no GPU; the pointers are never
+dereferenced), and their workspace sizes."""
+import ctypes
+
+import pytest
+
+import tree_speculative_decoding_jt_gb300 as jt
+
+A, B, C = (ctypes.c_void_p(4096 * i) for i in (1, 2, 3))
+ODD = ctypes.c_void_p(4096 + 8)
+INVALID, UNSUPPORTED, WORKSPACE = jt.JT_ERR_INVALID, jt.JT_ERR_UNSUPPORTED, jt.JT_ERR_WORKSPACE
+
+
+def call(name, defaults, **change):
+    assert set(change) <= set(defaults), change
+    args = {**defaults, **change}
+    return getattr(jt.load(), name)(*args.values())
+
+
+APPEND = dict(qkv=A, dtype=1, row_stride=6144, q_weight=None, k_weight=None, eps=1e-6, cos_sin=A, max_pos=100,
+              rot_dim=128, interleaved=0, depth=None, block_table=A, max_pages=4, num_pages=9, prefix_len=A, tree_off=A,
+              nseq=2, total=5, Hq=32, Hkv=8, D=128, page_size=16, q_out=A, k_cache=A, v_cache=A, ws=A, ws_bytes=0,
+              stream=None)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(qkv=None), INVALID), (dict(q_out=None), INVALID), (dict(k_cache=None), INVALID), (dict(v_cache=None), INVALID),
+    (dict(block_table=None), INVALID), (dict(prefix_len=None), INVALID), (dict(tree_off=None), INVALID),
+    (dict(cos_sin=None), INVALID), (dict(max_pos=0), INVALID), (dict(row_stride=6136), INVALID),
+    (dict(row_stride=6148), INVALID), (dict(qkv=ODD), INVALID), (dict(k_weight=ODD), INVALID), (dict(cos_sin=ODD), INVALID),
+    (dict(q_out=ODD), INVALID), (dict(v_cache=ODD), INVALID), (dict(nseq=0), INVALID), (dict(nseq=65536), INVALID),
+    (dict(total=-1), INVALID), (dict(Hq=-1), INVALID), (dict(Hkv=0), INVALID), (dict(page_size=32), INVALID),
+    (dict(dtype=2), INVALID), (dict(rot_dim=144), INVALID), (dict(rot_dim=-16), INVALID), (dict(interleaved=2), INVALID),
+    (dict(eps=-1.0), INVALID), (dict(eps=float("nan")), INVALID), (dict(max_pages=0), INVALID), (dict(num_pages=0), INVALID),
+    (dict(D=96, rot_dim=96), UNSUPPORTED), (dict(rot_dim=120), UNSUPPORTED), (dict(dtype=0, D=48), INVALID),
+    (dict(dtype=0, D=48, rot_dim=8), UNSUPPORTED), (dict(dtype=0, rot_dim=12), UNSUPPORTED),
+    (dict(), WORKSPACE), (dict(ws=None, ws_bytes=256), WORKSPACE), (dict(ws=ODD, ws_bytes=256), WORKSPACE),
+    (dict(total=0), jt.JT_OK), (dict(total=0, qkv=None, q_out=None), jt.JT_OK),
+])
+def test_append_refusals(change, status):
+    assert call("jt_qkv_append", APPEND, **change) == status
+
+
+CHUNK = dict(q=A, k_cache=A, v_cache=A, dtype=1, block_table=A, max_pages=4, num_pages=9, prefix_len=A, chunk_off=A,
+             nseq=2, total=5, max_chunk=4, Hq=32, Hkv=8, D=128, page_size=16, scale=0.1, out=A, lse=None, ws=A,
+             ws_bytes=0, stream=None)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(q=None), INVALID), (dict(k_cache=None), INVALID), (dict(v_cache=None), INVALID), (dict(out=None), INVALID),
+    (dict(block_table=None), INVALID), (dict(prefix_len=None), INVALID), (dict(chunk_off=None), INVALID),
+    (dict(q=ODD), INVALID), (dict(out=ODD), INVALID), (dict(k_cache=ODD), INVALID), (dict(nseq=0), INVALID),
+    (dict(nseq=65536), INVALID), (dict(total=-1), INVALID), (dict(max_chunk=0), INVALID), (dict(Hq=33), INVALID),
+    (dict(Hkv=0), INVALID), (dict(page_size=8), INVALID), (dict(scale=float("inf")), INVALID), (dict(dtype=3), INVALID),
+    (dict(max_pages=0), INVALID), (dict(num_pages=0), INVALID), (dict(D=96), UNSUPPORTED), (dict(D=256), UNSUPPORTED),
+    (dict(dtype=0, D=80), UNSUPPORTED), (dict(Hq=129, Hkv=1), UNSUPPORTED), (dict(dtype=0, Hq=65, Hkv=1), UNSUPPORTED),
+    (dict(dtype=0, nseq=65535, Hq=64, Hkv=64, max_chunk=1 << 30), UNSUPPORTED),
+    (dict(), WORKSPACE), (dict(dtype=0), WORKSPACE), (dict(ws=None, ws_bytes=1 << 30), WORKSPACE),
+    (dict(ws=ODD, ws_bytes=1 << 30), WORKSPACE), (dict(total=0), jt.JT_OK), (dict(total=0, q=None, out=None), jt.JT_OK),
+])
+def test_chunk_refusals(change, status):
+    assert call("jt_chunk_attn_paged", CHUNK, **change) == status
+
+
+COMMIT = dict(k_cache=A, v_cache=A, dtype=1, layers=2, layer_stride=9 * 16 * 8 * 128, block_table=A, max_pages=4,
+              num_pages=9, prefix_len=A, tree_off=A, accept_len=A, path=A, nseq=2, N=8, Hkv=8, D=128, page_size=16,
+              new_prefix=B, ws=C, ws_bytes=0, stream=None)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(k_cache=None), INVALID), (dict(v_cache=None), INVALID), (dict(block_table=None), INVALID),
+    (dict(prefix_len=None), INVALID), (dict(tree_off=None), INVALID), (dict(accept_len=None), INVALID),
+    (dict(path=None), INVALID), (dict(new_prefix=None), INVALID), (dict(k_cache=ODD), INVALID), (dict(nseq=0), INVALID),
+    (dict(nseq=65536), INVALID), (dict(N=-1), INVALID), (dict(N=257), INVALID), (dict(layers=0), INVALID),
+    (dict(layer_stride=9 * 16 * 8 * 128 - 8), INVALID), (dict(layer_stride=9 * 16 * 8 * 128 + 4), INVALID),
+    (dict(page_size=64), INVALID), (dict(dtype=5), INVALID), (dict(Hkv=0), INVALID), (dict(D=0), INVALID),
+    (dict(new_prefix=ctypes.c_void_p(4096 + 4)), INVALID),  # overlaps prefix_len in part
+    (dict(Hkv=1, D=4, layers=1), UNSUPPORTED), (dict(Hkv=3, D=7, layers=1, dtype=0), UNSUPPORTED),
+    (dict(), WORKSPACE), (dict(new_prefix=A, ws_bytes=256), WORKSPACE), (dict(ws=None, ws_bytes=4096), WORKSPACE),
+])
+def test_commit_refusals(change, status):
+    assert call("jt_kv_commit", COMMIT, **change) == status
+
+
+def test_workspace_sizes():
+    size = jt.jt_workspace_size
+    assert size(jt.JT_OP_QKV_APPEND) == 256
+    assert size(jt.JT_OP_KV_COMMIT, 1) == 512 and size(jt.JT_OP_KV_COMMIT, 65) == 768
+    assert size(jt.JT_OP_KV_COMMIT, 0) == 0
+    assert size(jt.JT_OP_CHUNK_ATTN, 2, 0, 0, 0, 5, 32, 8, 128, 4, 4) > 4096
+    assert size(jt.JT_OP_CHUNK_ATTN, 2, 0, 0, 0, 5, 33, 8, 128, 4, 4) == 0
+
+
+def test_binding_refuses_cpu_tensors_and_wrong_shapes():
+    import torch
+
+    z = torch.zeros
+    i32 = dict(dtype=torch.int32)
+    k = z(3, 16, 2, 64)
+    with pytest.raises(ValueError):
+        jt.jt_qkv_append(z(4, 8 * 64), 4, k, k, z(1, 2, **i32), z(1, **i32), z(2, **i32))
+    with pytest.raises(ValueError):
+        jt.jt_chunk_attn_paged(z(4, 4, 64), k, k, z(1, 2, **i32), z(1, **i32), z(2, **i32), max_chunk=4)
+    with pytest.raises(ValueError):
+        jt.jt_kv_commit(k, k, z(1, 2, **i32), z(1, **i32), z(2, **i32), z(1, **i32), z(1, 3, **i32))
+    with pytest.raises(TypeError):
+        jt.jt_chunk_attn_paged(z(4, 4, 64).half(), k, k, z(1, 2, **i32), z(1, **i32), z(2, **i32), max_chunk=4)
+
+
+def test_rope_table():
+    import math
+
+    t = jt.rope_table(1001, 16, theta=1e4, device="cpu")
+    assert t.shape == (1001, 16)
+    for pos in (0, 1, 1000):
+        for j in range(8):
+            a = pos * 1e4 ** (-2 * j / 16)
+            assert abs(t[pos, j].item() - math.cos(a)) <= 2 ** -24 and abs(t[pos, 8 + j].item() - math.sin(a)) <= 2 ** -24

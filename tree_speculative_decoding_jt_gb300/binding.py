@@ -23,14 +23,15 @@ JT_OK, JT_ERR_INVALID, JT_ERR_UNSUPPORTED, JT_ERR_CUDA, JT_ERR_TIMEOUT, JT_ERR_W
 JT_DTYPE_F32, JT_DTYPE_BF16 = 0, 1
 JT_RULE_GREEDY, JT_RULE_MARGIN = 0, 1
 (JT_OP_TREE_BUILD, JT_OP_TREE_ATTN, JT_OP_VERIFY_ACCEPT, JT_OP_TREE_TOPW, JT_OP_TREE_BUILD_MIXED,
- JT_OP_TREE_POLICY) = 0, 1, 2, 3, 4, 5
+ JT_OP_TREE_POLICY, JT_OP_CHUNK_ATTN, JT_OP_KV_COMMIT, JT_OP_QKV_APPEND) = range(9)
 JT_MAX_TREE, JT_MAX_W, JT_MAX_N, JT_PAGE_SIZE = 256, 8, 64, 16
 
 # every symbol include/jt.h declares
 EXPORTS = ("jt_workspace_size", "jt_tree_build", "jt_tree_topw", "jt_tree_expand",
            "jt_tree_attn_paged", "jt_verify_accept", "jt_check", "jt_status_str", "jt_version",
            "jt_tree_build_noalloc", "jt_verify_accept_stochastic", "jt_tree_build_mixed",
-           "jt_tree_expand_capped", "jt_tree_policy", "jt_tree_build_adaptive", "jt_selftest_wait_timeout")
+           "jt_tree_expand_capped", "jt_tree_policy", "jt_tree_build_adaptive", "jt_selftest_wait_timeout",
+           "jt_qkv_append", "jt_chunk_attn_paged", "jt_kv_commit")
 
 _lock = threading.Lock()
 _lib = None
@@ -105,6 +106,12 @@ def load(build_if_missing: bool = True):
         lib.jt_verify_accept.argtypes = [P, P, P, P, i32, i32, i64, i32, i32, f64, P, P, P, P, sz, P]
         lib.jt_verify_accept_stochastic.argtypes = [P, P, P, P, P, i32, i32, i64, i32, P, P, P, P, P,
                                                     P, sz, P]
+        lib.jt_qkv_append.argtypes = [P, i32, i64, P, P, f32, P, i32, i32, i32, P, P, i32, i32, P, P, i32, i32,
+                                      i32, i32, i32, i32, P, P, P, P, sz, P]
+        lib.jt_chunk_attn_paged.argtypes = [P, P, P, i32, P, i32, i32, P, P, i32, i32, i32, i32, i32, i32, i32,
+                                            f32, P, P, P, sz, P]
+        lib.jt_kv_commit.argtypes = [P, P, i32, i32, i64, P, i32, i32, P, P, P, P, i32, i32, i32, i32, i32, P, P,
+                                     sz, P]
         lib.jt_check.argtypes = [P, P]
         lib.jt_selftest_wait_timeout.argtypes = [P, sz, P]
         lib.jt_status_str.argtypes = [i32]
@@ -113,7 +120,8 @@ def load(build_if_missing: bool = True):
         for name in ("jt_tree_build", "jt_tree_topw", "jt_tree_expand", "jt_tree_attn_paged",
                      "jt_verify_accept", "jt_check", "jt_version", "jt_tree_build_noalloc",
                      "jt_verify_accept_stochastic", "jt_tree_build_mixed", "jt_tree_expand_capped",
-                     "jt_tree_policy", "jt_tree_build_adaptive", "jt_selftest_wait_timeout"):
+                     "jt_tree_policy", "jt_tree_build_adaptive", "jt_selftest_wait_timeout", "jt_qkv_append",
+                     "jt_chunk_attn_paged", "jt_kv_commit"):
             getattr(lib, name).restype = i32
         _lib = lib
         return lib
@@ -528,6 +536,176 @@ def jt_verify_accept(target_logits, parent, token, tree_off, N, rule=JT_RULE_GRE
                               _ptr(ws), ws.numel(), _stream(stream))
     _check(rc, "jt_verify_accept")
     return acc, path, bonus
+
+
+def _dtype_of(t, name):
+    if t.dtype == torch.bfloat16:
+        return JT_DTYPE_BF16
+    if t.dtype == torch.float32:
+        return JT_DTYPE_F32
+    raise TypeError(f"{name} must be bf16 or fp32")
+
+
+def _shape(t, name, shape):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    return t
+
+
+def _caches(k_cache, v_cache, dtype, dims=(4,)):
+    _need(k_cache, "k_cache", dtype)
+    _need(v_cache, "v_cache", dtype)
+    if k_cache.dim() not in dims:
+        raise ValueError(f"k_cache must have {' or '.join(map(str, dims))} dimensions, got {k_cache.dim()}")
+    _shape(v_cache, "v_cache", k_cache.shape)
+
+
+def _batch(block_table, prefix_len, off, off_name):
+    _need(block_table, "block_table", torch.int32)
+    _need(prefix_len, "prefix_len", torch.int32)
+    _need(off, off_name, torch.int32)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must have 2 dimensions")
+    nseq, max_pages = block_table.shape
+    _shape(prefix_len, "prefix_len", (nseq,))
+    _shape(off, off_name, (nseq + 1,))
+    return nseq, max_pages
+
+
+def rope_table(max_pos, rot_dim, theta=1e6, device=None):
+    """cos_sin table of jt_qkv_append for the usual angles pos * theta^(-2j /
+    rot_dim): fp32 [max_pos, rot_dim], cosines then sines, computed in 64 bits
+    and rounded once (made once per model)."""
+    inv = float(theta) ** (-torch.arange(0, rot_dim, 2, dtype=torch.float64) / rot_dim)
+    a = torch.arange(max_pos, dtype=torch.float64)[:, None] * inv
+    return torch.cat([a.cos(), a.sin()], 1).float().to(device or "cuda")
+
+
+@_on_tensor_device
+def jt_qkv_append(qkv, Hq, k_cache, v_cache, block_table, prefix_len, tree_off, q_weight=None, k_weight=None,
+                  eps=1e-6, cos_sin=None, interleaved=False, depth=None, q_out=None, ws=None, stream=None):
+    """Per-head norm of q and k, position rotation, and the write of k and v
+    into the paged cache, from the packed projection.
+
+    qkv [total, (Hq + 2 Hkv) * D] (rows may be strided); k/v_cache [pages, 16,
+    Hkv, D]; q_weight, k_weight [D] or None; cos_sin fp32 [max_pos, rot_dim] or
+    None (see rope_table); depth int32 [total] (tree nodes: position L_b +
+    depth) or None (position L_b + i).  Returns q_out [total, Hq, D] (None for
+    Hq = 0); the caches are updated in place."""
+    lib = load()
+    dtype = _dtype_of(qkv, "qkv")
+    if not qkv.is_cuda:
+        raise ValueError("qkv must be a CUDA tensor (libjt has no CPU path)")
+    _caches(k_cache, v_cache, qkv.dtype)
+    nseq, max_pages = _batch(block_table, prefix_len, tree_off, "tree_off")
+    num_pages, page, Hkv, D = k_cache.shape
+    if qkv.dim() != 2 or qkv.shape[1] != (Hq + 2 * Hkv) * D:
+        raise ValueError(f"qkv must be [total, (Hq + 2 Hkv) * D = {(Hq + 2 * Hkv) * D}], got {tuple(qkv.shape)}")
+    if qkv.stride(1) != 1:
+        raise ValueError("qkv's rows must be contiguous")
+    total = qkv.shape[0]
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _shape(_need(w, name, qkv.dtype), name, (D,))
+    max_pos = rot = 0
+    if cos_sin is not None:
+        _need(cos_sin, "cos_sin", torch.float32)
+        if cos_sin.dim() != 2:
+            raise ValueError("cos_sin must be [max_pos, rot_dim]")
+        max_pos, rot = cos_sin.shape
+    if depth is not None:
+        _shape(_need(depth, "depth", torch.int32), "depth", (total,))
+    if q_out is None and Hq > 0:
+        q_out = torch.empty((total, Hq, D), dtype=qkv.dtype, device=qkv.device)
+    elif q_out is not None:
+        _shape(_need(q_out, "q_out", qkv.dtype), "q_out", (total, Hq, D))
+    if ws is None:
+        ws = workspace(jt_workspace_size(JT_OP_QKV_APPEND), qkv.device)
+    # a single row's stride is whatever the view says: any value that fits does
+    rc = lib.jt_qkv_append(_ptr(qkv), dtype, qkv.stride(0) if total > 1 else qkv.shape[1], _ptr(q_weight),
+                           _ptr(k_weight), float(eps), _ptr(cos_sin), max_pos, rot, 1 if interleaved else 0,
+                           _ptr(depth), _ptr(block_table), max_pages, num_pages, _ptr(prefix_len), _ptr(tree_off),
+                           nseq, total, Hq, Hkv, D, page, _ptr(q_out), _ptr(k_cache), _ptr(v_cache), _ptr(ws),
+                           ws.numel(), _stream(stream))
+    _check(rc, "jt_qkv_append")
+    return q_out
+
+
+@_on_tensor_device
+def jt_chunk_attn_paged(q, k_cache, v_cache, block_table, prefix_len, chunk_off, scale=None, max_chunk=None,
+                        out=None, lse=None, ws=None, stream=None, with_lse=True):
+    """Causal attention of new tokens (chunks of any length, ragged) over a
+    paged KV cache that already holds their keys and values.
+
+    q [total, Hq, D]; k/v [pages, 16, Hkv, D] (both bf16, or both fp32);
+    block_table [nseq, max_pages] int32; prefix_len [nseq] int32 (tokens cached
+    before); chunk_off [nseq+1] int32; max_chunk: the longest chunk (an upper
+    bound; None reads it from chunk_off, which waits for the device).  Returns
+    (out, lse)."""
+    lib = load()
+    dtype = _dtype_of(q, "q")
+    _need(q, "q", None)
+    _caches(k_cache, v_cache, q.dtype)
+    nseq, max_pages = _batch(block_table, prefix_len, chunk_off, "chunk_off")
+    if q.dim() != 3:
+        raise ValueError("q must be [total, Hq, D]")
+    total, Hq, D = q.shape
+    num_pages, page, Hkv, D2 = k_cache.shape
+    if D2 != D:
+        raise ValueError("q and k_cache head dims differ")
+    if max_chunk is None:
+        max_chunk = max(1, int((chunk_off[1:] - chunk_off[:-1]).max().item()))
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _shape(_need(out, "out", q.dtype), "out", q.shape)
+    if lse is None and with_lse:
+        lse = torch.empty((total, Hq), dtype=torch.float32, device=q.device)
+    elif lse is not None:
+        _shape(_need(lse, "lse", torch.float32), "lse", (total, Hq))
+    if ws is None:
+        ws = workspace(jt_workspace_size(JT_OP_CHUNK_ATTN, nseq, 0, 0, 0, total, Hq, Hkv, D, max_pages, max_chunk),
+                       q.device)
+    rc = lib.jt_chunk_attn_paged(_ptr(q), _ptr(k_cache), _ptr(v_cache), dtype, _ptr(block_table), max_pages,
+                                 num_pages, _ptr(prefix_len), _ptr(chunk_off), nseq, total, max_chunk, Hq, Hkv, D,
+                                 page, float(scale), _ptr(out), _ptr(lse), _ptr(ws), ws.numel(), _stream(stream))
+    _check(rc, "jt_chunk_attn_paged")
+    return out, lse
+
+
+@_on_tensor_device
+def jt_kv_commit(k_cache, v_cache, block_table, prefix_len, tree_off, accept_len, path, new_prefix=None, ws=None,
+                 stream=None):
+    """Move the accepted path's keys and values behind the prefix and advance
+    the prefix lengths.
+
+    k/v_cache [pages, 16, Hkv, D] or [layers, pages, 16, Hkv, D] (bf16 or fp32,
+    updated in place); accept_len [nseq], path [nseq, N+1] int32 as
+    jt_verify_accept returns them; new_prefix: int32 [nseq] output, prefix_len
+    itself to update it in place, None for a new tensor.  Returns new_prefix."""
+    lib = load()
+    dtype = _dtype_of(k_cache, "k_cache")
+    _caches(k_cache, v_cache, k_cache.dtype, (4, 5))
+    nseq, max_pages = _batch(block_table, prefix_len, tree_off, "tree_off")
+    _shape(_need(accept_len, "accept_len", torch.int32), "accept_len", (nseq,))
+    _need(path, "path", torch.int32)
+    if path.dim() != 2 or path.shape[0] != nseq:
+        raise ValueError(f"path must be [{nseq}, N+1]")
+    num_pages, page, Hkv, D = k_cache.shape[-4:]
+    layers = k_cache.shape[0] if k_cache.dim() == 5 else 1
+    if new_prefix is None:
+        new_prefix = torch.empty_like(prefix_len)
+    else:
+        _shape(_need(new_prefix, "new_prefix", torch.int32), "new_prefix", (nseq,))
+    if ws is None:
+        ws = workspace(jt_workspace_size(JT_OP_KV_COMMIT, nseq), k_cache.device)
+    rc = lib.jt_kv_commit(_ptr(k_cache), _ptr(v_cache), dtype, layers, num_pages * page * Hkv * D, _ptr(block_table),
+                          max_pages, num_pages, _ptr(prefix_len), _ptr(tree_off), _ptr(accept_len), _ptr(path), nseq,
+                          path.shape[1] - 1, Hkv, D, page, _ptr(new_prefix), _ptr(ws), ws.numel(), _stream(stream))
+    _check(rc, "jt_kv_commit")
+    return new_prefix
 
 
 @_on_tensor_device

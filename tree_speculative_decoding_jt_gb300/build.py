@@ -31,7 +31,8 @@ def lib_path(variant: str = "") -> str:
     if variant not in VARIANTS:
         raise ValueError(f"unknown libjt variant {variant!r} (known: {sorted(VARIANTS)})")
     return LIB if not variant else os.path.join(HERE, f"libjt_{variant}.so")
-SOURCES = ["jt_api.cu", "tree_build.cu", "verify_accept.cu", "tree_attn.cu", "tree_attn_f32.cu", "jt_noalloc.cu", "verify_stochastic.cu", "jt_selftest.cu"]
+SOURCES = ["jt_api.cu", "tree_build.cu", "verify_accept.cu", "tree_attn.cu", "tree_attn_f32.cu", "jt_noalloc.cu", "verify_stochastic.cu", "jt_selftest.cu",
+           "chunk_attn.cu", "chunk_attn_f32.cu", "kv_cache.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-Xptxas", "-warn-spills"]

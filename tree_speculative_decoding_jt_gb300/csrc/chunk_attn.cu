@@ -1,0 +1,1325 @@
+// chunk_attn.cu -- causal attention of a ragged batch of new tokens over a
+// paged bf16 KV cache on the sm_103a tensor cores (tcgen05 + TMEM + TMA).
+//
+// Mathematics.  Sequence b has L_b cached tokens and B_b new ones, whose keys
+// and values already sit in the slots L_b .. L_b + B_b - 1.  New token i sees
+// the slots 0 .. L_b + i:
+//     out = sum_s exp(scale q.k_s - m) v_s / l,  l = sum_s exp(scale q.k_s - m),
+// one pass over the keys with the running maximum m and sum l (fp32), P =
+// exp(...) rounded to bf16 for the second product (relative 2^-9 each, the
+// rounding of the inputs themselves; l sums the unrounded values), the output
+// rounded once.
+//
+// Work.  A unit is (sequence b, KV head g, query-tile pair mp): two 128-row
+// query tiles of npt = 128 / G new tokens x the G query heads of KV head g
+// (stacked in the MMA's M dimension: they share K and V) against the 128-key
+// tiles 0 .. T_u - 1 of the keys that the pair's last token sees.  A work slot
+// is a pair of CTAs on two SMs (a cluster): CTA rank X takes query tile X, and
+// one tcgen05.mma.cta_group::2 of M = 256 covers both.  Each CTA holds its half
+// of every K tile (keys 64X..) and of every V tile (dims D/2 X..), so a unit's
+// keys cross L2 once for 256 query rows.  All units' key tiles are laid end to
+// end in (b, g, mp) order and cut into one equal range per work slot, planned
+// on the device from prefix_len and chunk_off (sums over a head's units in
+// closed form), so lengths never visit the host and every SM gets the same
+// number of tiles.  A unit cut by a range boundary leaves fp32 partials; the
+// slot that finishes its last piece merges them, summing in piece order.
+//
+// Warps per CTA (384 threads; warp 11 idles):
+//   0-3 / 4-7  softmax of the tiles with even / odd number, one query row per
+//              thread.  Warps w and w + 4 hold the same 32 rows: the running
+//              maximum of a row goes from one to the other through shared
+//              memory, tile by tile (m_bar), and each keeps its own part of
+//              the sum.  So each warp has two tiles' time for one tile's
+//              softmax, which a single warp per row had not: the tensor pipe
+//              sets the pace.  O is rescaled only when a row's maximum grows by
+//              more than 2^32: P then stays below 2^32 and O and l far inside
+//              fp32.  Warps whose rows are all past the chunk's end (single
+//              tokens fill 1 to 16 of 256 rows) compute nothing.
+//   8 / 10     TMA producers of Q and K / of V, one box per 16-token page;
+//   9          TMEM allocation; in the pair's leader, the MMA issuer.
+// TMEM (512 columns): S0, S1, S2 (P of a tile overwrites the first half of its
+// S) and O.  The MMA warp issues QK up to three tiles ahead, across units; Q
+// is double buffered.
+#include <algorithm>
+
+#include "jt_common.cuh"
+#include "jt_internal.h"
+
+namespace jt {
+namespace chunk {
+
+constexpr int kThreads = 384;
+// Registers: 168 a thread at launch (three warps per SM quarter); the softmax
+// warps, which hold a whole score row, take what the others give up: 256 * 208
+// + 128 * 88 = 384 * 168.
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
+constexpr int kTileN = 128;  // keys per KV tile
+constexpr int kTileM = 128;  // query rows per query tile
+constexpr float kRescaleLog2 = 32.0f;
+
+struct Params {
+    const int32_t* block_table;
+    const int32_t* prefix_len;
+    const int32_t* off;
+    const __nv_bfloat16* q;
+    const __nv_bfloat16* k_cache;
+    const __nv_bfloat16* v_cache;
+    __nv_bfloat16* out;
+    float* lse;
+    float* part_o;    // [2 * slots][2][128][D]: partial O of the pieces of cut units
+    float2* part_ml;  // [2 * slots][2][128]: their running max (log2 units) and sum
+    unsigned long long* tickets;    // CTA arrivals over all calls (workspace header)
+    unsigned long long* merge_cnt;  // [slots][2]: (call number << 32) | pieces done
+    uint32_t* err;
+    int max_pages, num_pages, nseq, total, max_chunk, Hq, Hkv, G, npt;
+    float scale_log2;
+};
+
+template <int D>
+struct Smem {
+    static constexpr int kChunks = D / 64;                  // 64-dim (128-byte) column blocks of Q and K
+    static constexpr int kQChunk = kTileM * 128;            // 128 query rows x 64 dims
+    static constexpr int kQBytes = kChunks * kQChunk;
+    static constexpr int kKChunk = 64 * 128;                // 64 keys x 64 dims
+    static constexpr int kKHalf = kChunks * kKChunk;        // this CTA's 64 keys
+    static constexpr int kVRow = D;                         // bytes of this CTA's D / 2 dims of one key
+    static constexpr int kVHalf = kTileN * kVRow;
+    static constexpr int kKStages = D == 128 ? 4 : 6;
+    static constexpr int kVStages = D == 128 ? 4 : 6;
+    static constexpr int kQ = 0;                            // two Q tiles
+    static constexpr int kK = kQ + 2 * kQBytes;
+    static constexpr int kV = kK + kKStages * kKHalf;
+    static constexpr int kStage = kV + kVStages * kVHalf;   // epilogue staging, 2 KB per softmax warp
+    static constexpr int kBar = kStage + 8 * 2048;
+    static constexpr int kM = kBar + 512;                   // running maxima [tile parity][row]
+    static constexpr int kX = kM + 1024;                    // (max, sum) [row / 32][piece parity][warpgroup][lane]
+    static constexpr int kBytes = kX + 4096;
+    static constexpr int kAlloc = kBytes + 1024;            // room to align the base to 1024
+};
+
+constexpr int kMaxStages = 6;
+
+struct Bars {
+    uint64_t q_full[2];             // leader: both CTAs' Q tiles have landed
+    uint64_t q_empty[2];            // every QK of the piece has completed
+    uint64_t k_full[kMaxStages];    // leader: both halves of the stage's K tile have landed
+    uint64_t k_empty[kMaxStages];   // QK of the stage's tile has completed
+    uint64_t v_full[kMaxStages];    // leader: both halves of the stage's V tile have landed
+    uint64_t v_empty[kMaxStages];   // PV of the stage's tile has completed
+    uint64_t v_own[kMaxStages];     // this CTA's half of a unit-final V tile has landed
+    uint64_t s_full[3];             // S buffer holds QK of its latest tile
+    uint64_t p_full[3];             // leader: P of the tile in the S buffer, from 8 softmax warps
+    uint64_t o_done[3];             // one phase per PV of a tile t with t mod 3 == index
+    uint64_t o_free;                // leader: the pair's 16 softmax warps have read the piece's O
+    uint64_t mma_final;             // every MMA of the pair has completed
+    uint64_t m_bar[4][2];           // warps w, w + 4: the running maxima after a tile of this parity
+    uint64_t x_bar[4];              // warps w, w + 4 meet at the end of a piece
+    uint64_t msync;                 // this CTA's 8 softmax warps meet (merge of a cut unit)
+    uint32_t tmem_base;
+    int abort;
+    int w_b, w_g, w_mp, w_t, w_quota, w_P;
+    uint32_t call_id;
+    int merge_flag;
+};
+static_assert(sizeof(Bars) <= 512, "barrier block");
+
+// ---------------------------------------------------------------------------
+// The work plan
+// ---------------------------------------------------------------------------
+struct SeqInfo {
+    int L, B, off;
+    int np;  // query-tile pairs (0: no new token, -1: contents out of range)
+};
+
+__device__ __forceinline__ SeqInfo load_seq(const Params& p, int b) {
+    SeqInfo s;
+    s.off = p.off[b];
+    s.B = p.off[b + 1] - s.off;
+    s.L = p.prefix_len[b];
+    const bool ok = s.B >= 0 && s.B <= p.max_chunk && s.L >= 0 && s.off >= 0 && s.off <= p.total - s.B &&
+                    static_cast<long long>(s.L) + s.B <=
+                        min(static_cast<long long>(p.max_pages) * JT_PAGE_SIZE, 0x7FFFFF00ll);
+    s.np = !ok ? -1 : (s.B + 2 * p.npt - 1) / (2 * p.npt);
+    return s;
+}
+
+// Keys needed by pair mp: those its last token sees.
+__device__ __forceinline__ int unit_end(const SeqInfo& s, int mp, int npt) {
+    return s.L + min(s.B, (mp + 1) * 2 * npt);
+}
+__device__ __forceinline__ int unit_tiles(const SeqInfo& s, int mp, int npt) {
+    return static_cast<int>((static_cast<unsigned>(unit_end(s, mp, npt)) + kTileN - 1u) / kTileN);
+}
+
+// sum_{i=0}^{n-1} floor((a i + b) / m), by the Euclidean reduction of (a, m).
+__device__ __noinline__ long long floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
+    long long ans = 0;
+    for (;;) {
+        if (a >= m) {
+            ans += static_cast<long long>(n) * (n - 1) / 2 * (a / m);
+            a %= m;
+        }
+        if (b >= m) {
+            ans += static_cast<long long>(n) * (b / m);
+            b %= m;
+        }
+        const uint32_t y = a * n + b;  // a, b < m <= 256: no overflow for n < 2^23
+        if (y < m) return ans;
+        n = y / m;
+        b = y % m;
+        const uint32_t t = m;
+        m = a;
+        a = t;
+    }
+}
+
+// Key tiles of the first k units of one KV head, k < np (each of 2 npt tokens).
+__device__ __forceinline__ long long prefix_tiles(const SeqInfo& s, int k, int npt) {
+    if (k <= 0) return 0;
+    return floor_sum(static_cast<uint32_t>(k), kTileN, 2u * npt, static_cast<uint32_t>(s.L) + kTileN - 1u + 2u * npt);
+}
+__device__ __forceinline__ long long head_tiles(const SeqInfo& s, int npt) {
+    if (s.np <= 0) return 0;
+    return prefix_tiles(s, s.np - 1, npt) + unit_tiles(s, s.np - 1, npt);
+}
+
+// One piece: key tiles [t0, t0 + nt) of unit (b, g, mp), which has T tiles.
+// slot: the partial slot the piece writes, or -1 when it is the whole unit.
+struct Piece {
+    SeqInfo s;
+    int b, g, mp, t0, nt, T, slot;
+    int gpos;  // global tile index of the piece's first tile
+};
+
+// Walks the pieces of one work slot's range in order; every role runs its own.
+struct Walker {
+    SeqInfo s;
+    int b, g, mp, t, remaining, piece, gpos, work;
+
+    __device__ __forceinline__ void init(const Params& p, const Bars* bars, int work_slot) {
+        b = bars->w_b;
+        g = bars->w_g;
+        mp = bars->w_mp;
+        t = bars->w_t;
+        remaining = bars->w_quota;
+        work = work_slot;
+        gpos = work * bars->w_P;
+        piece = 0;
+        if (remaining > 0) s = load_seq(p, b);
+    }
+
+    __device__ __forceinline__ bool next(const Params& p, Piece& pc) {
+        if (remaining <= 0) return false;
+        const int T = unit_tiles(s, mp, p.npt);
+        const int nt = min(T - t, remaining);
+        pc.s = s;
+        pc.b = b;
+        pc.g = g;
+        pc.mp = mp;
+        pc.t0 = t;
+        pc.nt = nt;
+        pc.T = T;
+        pc.slot = (t == 0 && nt == T) ? -1 : 2 * work + (piece == 0 ? 0 : 1);
+        pc.gpos = gpos;
+        gpos += nt;
+        remaining -= nt;
+        t += nt;
+        ++piece;
+        if (t == T && remaining > 0) {  // on to the next unit in (b, g, mp) order
+            t = 0;
+            if (++mp >= s.np) {
+                mp = 0;
+                if (++g >= p.Hkv) {
+                    g = 0;
+                    do {
+                        ++b;
+                        s = load_seq(p, b);
+                    } while (s.np <= 0 && b + 1 < p.nseq);
+                }
+            }
+        }
+        return true;
+    }
+};
+
+__device__ __forceinline__ long long warp_sum(long long v) {
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
+}
+
+// The planner (one warp): the total tile count, the range of work slot `work`
+// (of nwork) and the unit and tile that it starts at.  rec: also report the
+// sequences whose offsets or lengths are out of range.
+__device__ void plan_slot(const Params& p, Bars* bars, int lane, int work, int nwork, bool rec) {
+    long long total = 0;
+    for (int base = 0; base < p.nseq; base += 32) {
+        const int b = base + lane;
+        long long t = 0;
+        if (b < p.nseq) {
+            const SeqInfo s = load_seq(p, b);
+            if (s.np < 0) {
+                if (rec) raise_error(p.err, DEVERR_INVALID);
+            } else {
+                t = p.Hkv * head_tiles(s, p.npt);
+            }
+        }
+        total += warp_sum(t);
+    }
+    if (total > 0x7FFFFFFFll) {  // beyond the int tile arithmetic: refuse the launch's work
+        if (rec && lane == 0) raise_error(p.err, DEVERR_INVALID);
+        total = 0;
+    }
+    const int T_total = static_cast<int>(total);
+    const int P = T_total > 0 ? (T_total + nwork - 1) / nwork : 0;
+    const long long start = static_cast<long long>(work) * P;
+    int quota = (start < T_total) ? static_cast<int>(min(static_cast<long long>(P), T_total - start)) : 0;
+    int found_b = -1, found_rel = 0;
+    long long acc = 0;
+    for (int base = 0; base < p.nseq && quota > 0 && found_b < 0; base += 32) {
+        const int b = base + lane;
+        long long t = 0;
+        if (b < p.nseq) {
+            const SeqInfo s = load_seq(p, b);
+            if (s.np > 0) t = p.Hkv * head_tiles(s, p.npt);
+        }
+        long long incl = t;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long u = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+            if (lane >= o) incl += u;
+        }
+        const long long excl = acc + incl - t;
+        const bool here = t > 0 && start >= excl && start < excl + t;
+        const unsigned m = __ballot_sync(0xFFFFFFFFu, here);
+        if (m) {
+            const int src = __ffs(m) - 1;
+            found_b = base + src;
+            found_rel = static_cast<int>(start - __shfl_sync(0xFFFFFFFFu, excl, src));
+        }
+        acc += __shfl_sync(0xFFFFFFFFu, incl, 31);
+    }
+    if (found_b < 0) quota = 0;
+    int g = 0, mp = 0, t = 0;
+    if (quota > 0) {
+        const SeqInfo s = load_seq(p, found_b);
+        const int ht = static_cast<int>(head_tiles(s, p.npt));
+        g = found_rel / ht;
+        const int r = found_rel - g * ht;
+        int n = s.np;  // the last unit in [mp, mp + n) that starts at or before tile r
+        while (n > 1) {
+            const int step = (n + 31) / 32;
+            const bool le = lane * step < n && prefix_tiles(s, mp + lane * step, p.npt) <= r;
+            const unsigned m = __ballot_sync(0xFFFFFFFFu, le);
+            const int k = 31 - __clz(m | 1u);
+            mp += k * step;
+            n = min(step, n - k * step);
+        }
+        t = r - static_cast<int>(prefix_tiles(s, mp, p.npt));
+    }
+    if (lane == 0) {
+        bars->w_b = found_b;
+        bars->w_g = g;
+        bars->w_mp = mp;
+        bars->w_t = t;
+        bars->w_quota = quota;
+        bars->w_P = P;
+    }
+}
+
+// The slots holding the pieces of the unit that starts at global tile U and
+// has T tiles (range length P): c0 .. c0 + n - 1; partial slot of piece k.
+struct CutUnit {
+    int c0, n, slot0;
+    __device__ __forceinline__ CutUnit(int U, int T, int P) {
+        c0 = U / P;
+        n = (U + T - 1) / P - c0 + 1;
+        slot0 = 2 * c0 + (U == c0 * P ? 0 : 1);
+    }
+    __device__ __forceinline__ int slot(int k) const { return k == 0 ? slot0 : 2 * (c0 + k); }
+};
+
+// Call numbers for the merge counts: the first CTA of a call draws
+// kTicketQuantum - (CTAs - 1) tickets from the workspace's counter and every
+// other CTA one, so all CTAs of a call compute the same ticket /
+// kTicketQuantum, and counts left by earlier calls never need clearing.
+constexpr unsigned long long kTicketQuantum = 1ull << 24;
+
+__device__ __forceinline__ uint32_t draw_call_id(unsigned long long* tickets, bool first, unsigned ctas) {
+    const unsigned long long t = atomicAdd(tickets, first ? kTicketQuantum - (ctas - 1u) : 1ull);
+    return static_cast<uint32_t>(t / kTicketQuantum) + 1u;
+}
+
+// ---------------------------------------------------------------------------
+// softmax helpers: one query row (128 scores) per thread
+// ---------------------------------------------------------------------------
+struct SRow {
+    uint32_t c[4][32];
+};
+
+__device__ __forceinline__ void load_srow(uint32_t tS, SRow& s) {
+    tmem_ld32(tS, s.c[0]);
+    tmem_ld32(tS + 32, s.c[1]);
+    tmem_ld32(tS + 64, s.c[2]);
+    tmem_ld32(tS + 96, s.c[3]);
+    tmem_wait_ld();
+}
+
+// Columns at or past `visible` -> -inf.
+__device__ __forceinline__ void mask_srow(SRow& s, int visible) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int c = 0; c < 32; ++c)
+            if (32 * q + c >= visible) s.c[q][c] = __float_as_uint(-INFINITY);
+}
+
+__device__ __forceinline__ float ex2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Three-input maximum (one instruction on sm_100 and later).
+__device__ __forceinline__ float fmax3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// Packed fp32 pair arithmetic: (d0, d1) = (a0, a1) * (b0, b1) + (c0, c1), and the sum.
+__device__ __forceinline__ void ffma2(float& d0, float& d1, float a0, float a1, float b0, float b1, float c0,
+                                      float c1) {
+    asm("{\n\t.reg .b64 a, b, c, d;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d0), "=f"(d1)
+        : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c0), "f"(c1));
+}
+__device__ __forceinline__ void fadd2(float& d0, float& d1, float a0, float a1, float b0, float b1) {
+    asm("{\n\t.reg .b64 a, b, d;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d0), "=f"(d1)
+        : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+
+// Row maximum over eight independent chains.
+__device__ __forceinline__ float max_srow(const SRow& s) {
+    float m[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        m[i] = fmaxf(__uint_as_float(s.c[i >> 1][(i & 1) * 16]), __uint_as_float(s.c[i >> 1][(i & 1) * 16 + 1]));
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int c = 2; c < 16; c += 2)
+            m[i] = fmax3(m[i], __uint_as_float(s.c[i >> 1][(i & 1) * 16 + c]),
+                         __uint_as_float(s.c[i >> 1][(i & 1) * 16 + c + 1]));
+    return fmaxf(fmax3(m[0], m[1], m[2]), fmax3(fmax3(m[3], m[4], m[5]), m[6], m[7]));
+}
+
+// P = exp2(s * sl2 - m), packed to bf16 pairs into the first 64 columns of
+// the S region; returns the sum of the unrounded values.
+__device__ __forceinline__ float exp_store_srow(const SRow& s, uint32_t tS, float sl2, float m) {
+    float a0 = 0.0f, a1 = 0.0f, b0 = 0.0f, b1 = 0.0f;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+        uint32_t pk[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            const int c2 = (q & 1) * 8 + c;
+            float x0, x1;
+            ffma2(x0, x1, __uint_as_float(s.c[q >> 1][2 * c2]), __uint_as_float(s.c[q >> 1][2 * c2 + 1]), sl2, sl2,
+                  -m, -m);
+            const float e0 = ex2_approx(x0);
+            const float e1 = ex2_approx(x1);
+            if (c & 1)
+                fadd2(b0, b1, b0, b1, e0, e1);
+            else
+                fadd2(a0, a1, a0, a1, e0, e1);
+            pk[c] = pack_bf16x2(e0, e1);
+        }
+        tmem_st8(tS + 8 * q, pk);
+    }
+    return (a0 + a1) + (b0 + b1);
+}
+
+// Stage this warp's 32 rows' 16 * N-byte pieces (slot[N] = this thread's row)
+// through shared memory (16-byte slots XOR-swizzled by row) and store each
+// row's piece as whole lines: dst(rr) is where staged row rr goes (nullptr: skip).
+template <int N, typename Dst>
+__device__ __forceinline__ void stage_store(uint8_t* stage, int lane, const uint4 (&slot)[N], Dst dst) {
+    uint4* my_row = reinterpret_cast<uint4*>(stage + lane * (16 * N));
+#pragma unroll
+    for (int c = 0; c < N; ++c) my_row[c ^ (lane & (N - 1))] = slot[c];
+    __syncwarp();
+    const int sub = lane & (N - 1);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int rr = (32 / N) * i + lane / N;  // staged row this lane copies
+        const uint4 val = reinterpret_cast<const uint4*>(stage + rr * (16 * N))[sub ^ (rr & (N - 1))];
+        uint4* d = dst(rr);
+        if (d) d[sub] = val;
+    }
+    __syncwarp();  // the next piece overwrites the stage
+}
+
+// ---------------------------------------------------------------------------
+// Rows whose result is not finite.  A masked key has P = 0, but 0 times a
+// value that is not finite is not 0: the tensor core lets an infinity or NaN in
+// the values of a chunk's later token reach the rows before it in the same key
+// tile.  A row that comes out not finite is computed again here, key by key over
+// the keys that it sees (a warp per row): rare, and then right.
+// Columns [c0, c0 + 32 * kPer) of the row's output.
+// ---------------------------------------------------------------------------
+template <int D, int kPer>
+__device__ __noinline__ void redo_row(const Params& p, int b, int L, int g, int token, long long rowid, int c0,
+                                      int lane) {
+    constexpr int kQ = D / 32;
+    float qv[kQ], acc[kPer];
+#pragma unroll
+    for (int k = 0; k < kQ; ++k) qv[k] = __bfloat162float(p.q[rowid * D + lane + 32 * k]);
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) acc[k] = 0.0f;
+    float m = -INFINITY, l = 0.0f;
+    constexpr int kBatch = 8;  // keys in flight, half a page
+    for (int s0 = 0; s0 <= L + token; s0 += kBatch) {
+        const long long page = p.block_table[static_cast<long long>(b) * p.max_pages + s0 / JT_PAGE_SIZE];
+        const bool in_pool = page >= 0 && page < p.num_pages;  // the copies read zeros from a page outside
+        const long long base = ((page * JT_PAGE_SIZE + s0 % JT_PAGE_SIZE) * p.Hkv + g) * D;
+        const long long step = static_cast<long long>(p.Hkv) * D;
+        const int n = min(kBatch, L + token + 1 - s0);
+        float d[kBatch], v[kBatch][kPer];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            d[i] = 0.0f;
+            const bool on = in_pool && i < n;
+#pragma unroll
+            for (int k = 0; k < kQ; ++k)
+                d[i] = fmaf(qv[k], on ? __bfloat162float(p.k_cache[base + i * step + lane + 32 * k]) : 0.0f, d[i]);
+#pragma unroll
+            for (int k = 0; k < kPer; ++k)
+                v[i][k] = on ? __bfloat162float(p.v_cache[base + i * step + c0 + lane + 32 * k]) : 0.0f;
+        }
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1)
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) d[i] += __shfl_xor_sync(0xFFFFFFFFu, d[i], o);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            if (i >= n) break;
+            const float s = d[i] * p.scale_log2;
+            const float mn = fmaxf(m, s);
+            const float corr = m == -INFINITY ? 0.0f : exp2f(m - mn);
+            const float e = s == -INFINITY ? 0.0f : exp2f(s - mn);
+            l = l * corr + e;
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) acc[k] = fmaf(e, v[i][k], acc[k] * corr);
+            m = mn;
+        }
+    }
+    const float inv = 1.0f / l;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) p.out[rowid * D + c0 + lane + 32 * k] = __float2bfloat16(acc[k] * inv);
+}
+
+// Operand descriptors are stepped by adding the byte offset / 16 to the
+// start-address field.  The whole MMA warp calls these; one elected lane issues.
+
+// S (+)= Q K^T over the pair: D / 16 MMAs of M = 256, N = 128, K = 16.
+template <int D>
+__device__ __forceinline__ void issue_qk(uint32_t tS, uint64_t dq, uint64_t dk) {
+    using SL = Smem<D>;
+    constexpr uint32_t idesc = idesc_bf16_f32(2 * kTileM, kTileN, false);
+    if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t qo = ((kk >> 2) * SL::kQChunk + (kk & 3) * 32) >> 4;
+            const uint32_t ko = ((kk >> 2) * SL::kKChunk + (kk & 3) * 32) >> 4;
+            mma_ss_pair(tS, dq + qo, dk + ko, idesc, kk > 0 ? 1u : 0u);
+        }
+    }
+    __syncwarp();
+}
+
+// O (+)= P V over the pair, P (bf16 pairs) in the first 64 columns of an S
+// buffer: 8 MMAs of M = 256, N = D, K = 16.
+template <int D>
+__device__ __forceinline__ void issue_pv(uint32_t tO, uint32_t tP, uint64_t dv, bool accumulate) {
+    constexpr uint32_t idesc = idesc_bf16_f32(2 * kTileM, D, true);
+    if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < kTileN / 16; ++kk)
+            mma_ts_pair(tO, tP + kk * 8, dv + kk * ((16 * Smem<D>::kVRow) >> 4), idesc, (accumulate || kk > 0) ? 1u : 0u);
+    }
+    __syncwarp();
+}
+
+__device__ __forceinline__ void commit_warp(uint64_t* bar) {
+    if (elect_one()) mma_commit_pair(bar);
+    __syncwarp();
+}
+
+// MN-major B operand (V): 128-byte rows take the 128-byte swizzle (64 dims per
+// CTA), 64-byte rows the 64-byte one (32 dims per CTA); groups of 8 keys are
+// contiguous.
+template <int D>
+__device__ __forceinline__ uint64_t v_desc(uint32_t saddr) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
+    d |= static_cast<uint64_t>((Smem<D>::kVHalf >> 4) & 0x3FFFu) << 16;
+    d |= static_cast<uint64_t>((8 * Smem<D>::kVRow) >> 4) << 32;
+    d |= 1ull << 46;
+    d |= (D == 128 ? 2ull : 4ull) << 61;
+    return d;
+}
+
+// Page ids of 4 consecutive tiles (group g4) of a piece: lane l holds page
+// l % 8 of tile 4 * g4 + l / 8 of the piece.
+__device__ __forceinline__ int bt_group(const Params& p, const Piece& pc, int valid_end, int g4, int lane) {
+    const int tile = 4 * g4 + (lane >> 3);
+    const int slot = (pc.t0 + tile) * kTileN + (lane & 7) * JT_PAGE_SIZE;
+    return (tile < pc.nt && slot < valid_end)
+               ? p.block_table[static_cast<long long>(pc.b) * p.max_pages + slot / JT_PAGE_SIZE]
+               : 0;
+}
+
+// Merge of a cut unit's pieces for this CTA's query tile x: rows are dealt to
+// the 8 softmax warps, four at a time.  Per row M = max m_k, O = sum_k
+// 2^(m_k - M) O_k / sum_k 2^(m_k - M) l_k, in piece order whoever merges, so
+// every call rounds the same way.
+template <int D>
+__device__ __noinline__ void merge_rows(const Params& p, const Piece& pc, const CutUnit cu, int x, int swarp,
+                                        int lane) {
+    constexpr int kC = D / 32;  // columns per lane
+    const int tok0 = (2 * pc.mp + x) * p.npt;
+    const int rows = min(pc.s.B - tok0, p.npt) * p.G;
+    const int sub = lane & 7, rsub = lane >> 3;  // lane = (row of the batch, piece of the group)
+    for (int r0 = swarp * 4; r0 < rows; r0 += 32) {
+        const int myr = min(r0 + rsub, rows - 1);
+        auto prow = [&](int k, int r) {
+            return (static_cast<long long>(cu.slot(k)) * 2 + x) * kTileM + r;
+        };
+        float M = -INFINITY;
+        for (int k = sub; k < cu.n; k += 8) M = fmaxf(M, __ldcg(&p.part_ml[prow(k, myr)]).x);
+#pragma unroll
+        for (int o = 4; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
+        float acc[4][kC], lsum[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            lsum[i] = 0.0f;
+#pragma unroll
+            for (int c = 0; c < kC; ++c) acc[i][c] = 0.0f;
+        }
+        for (int k0 = 0; k0 < cu.n; k0 += 8) {
+            const float2 ml = k0 + sub < cu.n ? __ldcg(&p.part_ml[prow(k0 + sub, myr)]) : make_float2(-INFINITY, 0.0f);
+            const float w = ml.x == -INFINITY ? 0.0f : exp2f(ml.x - M);
+            const float wl = w * ml.y;
+            for (int k = 0; k < min(8, cu.n - k0); ++k) {
+                float v[4][kC];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float* src = p.part_o + prow(k0 + k, min(r0 + i, rows - 1)) * D + lane * kC;
+                    if (kC == 4) {
+                        const float4 f = __ldcg(reinterpret_cast<const float4*>(src));
+                        v[i][0] = f.x, v[i][1] = f.y, v[i][2 % kC] = f.z, v[i][3 % kC] = f.w;
+                    } else {
+                        const float2 f = __ldcg(reinterpret_cast<const float2*>(src));
+                        v[i][0] = f.x, v[i][1] = f.y;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float wk = __shfl_sync(0xFFFFFFFFu, w, 8 * i + k);
+                    lsum[i] += __shfl_sync(0xFFFFFFFFu, wl, 8 * i + k);
+                    // a piece without a visible key has weight 0, and O that nothing wrote to
+                    if (wk != 0.0f)
+#pragma unroll
+                        for (int c = 0; c < kC; ++c) acc[i][c] += wk * v[i][c];
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = r0 + i;
+            const float Mi = __shfl_sync(0xFFFFFFFFu, M, 8 * i);
+            if (r >= rows) continue;
+            const int token = tok0 + r / p.G;
+            const long long rowid = static_cast<long long>(pc.s.off + token) * p.Hq + pc.g * p.G + r % p.G;
+            const float inv = 1.0f / lsum[i];
+            float o[kC], probe = 0.0f;
+#pragma unroll
+            for (int c = 0; c < kC; ++c) {
+                o[c] = acc[i][c] * inv;
+                probe += o[c] * 0.0f;
+            }
+            __nv_bfloat16* dst = p.out + rowid * D + lane * kC;
+            if (kC == 4)
+                *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2 % kC], o[3 % kC]));
+            else
+                *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(o[0], o[1]);
+            if (lane == 0 && p.lse) p.lse[rowid] = (Mi + log2f(lsum[i])) * 0.6931471805599453f;
+            if (lsum[i] == lsum[i] && __any_sync(0xFFFFFFFFu, probe != 0.0f)) {
+                __syncwarp();
+                redo_row<D, kC>(p, pc.b, pc.s.L, pc.g, token, rowid, 0, lane);
+            }
+        }
+    }
+}
+
+template <int D>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    chunk_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                      const __grid_constant__ CUtensorMap tm_v, const Params p) {
+    using SL = Smem<D>;
+    constexpr int KS = SL::kKStages, VS = SL::kVStages;
+    constexpr int kHalfCols = D / 2;  // output columns per softmax warpgroup
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    Bars* bars = reinterpret_cast<Bars*>(smem + SL::kBar);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t rank = cluster_ctarank();  // 0: the leader, which issues the pair's MMAs
+    const int work = static_cast<int>(blockIdx.x >> 1), nwork = static_cast<int>(gridDim.x >> 1);
+    if (tid == 0) {
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&bars->q_full[s], 1);
+            mbar_init(&bars->q_empty[s], 1);
+        }
+        for (int s = 0; s < kMaxStages; ++s) {
+            mbar_init(&bars->k_full[s], 1);
+            mbar_init(&bars->k_empty[s], 1);
+            mbar_init(&bars->v_full[s], 1);
+            mbar_init(&bars->v_empty[s], 1);
+            mbar_init(&bars->v_own[s], 1);
+        }
+        for (int x = 0; x < 3; ++x) {
+            mbar_init(&bars->s_full[x], 1);
+            mbar_init(&bars->p_full[x], 8);
+            mbar_init(&bars->o_done[x], 1);
+        }
+        mbar_init(&bars->o_free, 16);
+        mbar_init(&bars->mma_final, 1);
+        for (int w = 0; w < 4; ++w) {
+            mbar_init(&bars->m_bar[w][0], 1);
+            mbar_init(&bars->m_bar[w][1], 1);
+            mbar_init(&bars->x_bar[w], 2);
+        }
+        mbar_init(&bars->msync, 8);
+        bars->abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 8 && lane == 0) {
+        tma_prefetch_desc(&tm_q);
+        tma_prefetch_desc(&tm_k);
+        tma_prefetch_desc(&tm_v);
+    }
+    if (warp == 9) tmem_alloc_pair(&bars->tmem_base, 512);
+    // The V ring starts as zeros, and the rows of a unit-final tile's last page
+    // past the needed slots are zeroed once it has landed: rows that no copy of
+    // the present tile wrote are then always finite (P is 0 there, but 0 * NaN
+    // would not be).
+    for (int i = tid; i < VS * SL::kVHalf / 16; i += kThreads)
+        reinterpret_cast<uint4*>(smem + SL::kV)[i] = make_uint4(0u, 0u, 0u, 0u);
+    fence_proxy_async_smem();
+    cluster_sync();  // both CTAs' barriers exist before any copy, commit or arrive crosses the pair
+    pdl_wait();      // no global memory is read before the previous kernel's writes are visible
+    if (warp == 8) plan_slot(p, bars, lane, work, nwork, work == 0 && rank == 0);
+    if (tid == 0) bars->call_id = draw_call_id(p.tickets, work == 0 && rank == 0, gridDim.x);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bars->tmem_base;
+    volatile int* abort = &bars->abort;
+    const int quota = bars->w_quota;  // the same in both CTAs: one plan per work slot
+
+    uint8_t* sQ = smem + SL::kQ;
+    uint8_t* sK = smem + SL::kK;
+    uint8_t* sV = smem + SL::kV;
+    const int npt = p.npt;
+
+    if (quota > 0 && warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        if (warp == 8) {
+            // ------------------------------------------------------- TMA: Q, K
+            Walker w;
+            w.init(p, bars, work);
+            Piece pc;
+            int jj = 0, npc = 0;
+            bool ok = true;
+            while (ok && !*abort && w.next(p, pc)) {
+                const int valid_end = unit_end(pc.s, pc.mp, npt);
+                const int qs = npc & 1;
+                // this CTA's Q tile (the peer's may lie past the chunk: its rows are never written out)
+                if (npc >= 2 && !mbar_wait_warp(&bars->q_empty[qs], ((npc >> 1) - 1) & 1, p.err, abort)) break;
+                if (lane == 0) {
+                    if (rank == 0) mbar_arrive_expect_tx(&bars->q_full[qs], 2 * SL::kChunks * npt * p.G * 128);
+                    for (int c = 0; c < SL::kChunks; ++c)
+                        tma_load_3d_pair(sQ + qs * SL::kQBytes + c * SL::kQChunk, &tm_q, cluster_map(&bars->q_full[qs], 0),
+                                         c * 64, pc.g * p.G, pc.s.off + (2 * pc.mp + static_cast<int>(rank)) * npt);
+                }
+                ++npc;
+                int bt_cur = bt_group(p, pc, valid_end, 0, lane);
+                int bt_nxt = bt_group(p, pc, valid_end, 1, lane);
+                int bt_nn = bt_group(p, pc, valid_end, 2, lane);
+                for (int j = 0; j < pc.nt; ++j, ++jj) {
+                    const int st = jj % KS;
+                    if (j > 0 && (j & 3) == 0) {
+                        bt_cur = bt_nxt;
+                        bt_nxt = bt_nn;
+                        bt_nn = bt_group(p, pc, valid_end, (j >> 2) + 2, lane);
+                    }
+                    const int nvalid = min(kTileN, valid_end - (pc.t0 + j) * kTileN);
+                    const int npg = (nvalid + JT_PAGE_SIZE - 1) / JT_PAGE_SIZE;
+                    const int pid = __shfl_sync(0xFFFFFFFFu, bt_cur, ((j & 3) << 3) + (lane & 7));
+                    JT_DCHECK(lane >= npg || (pid >= 0 && pid < p.num_pages), p.err);  // block-table entry in the pool
+                    // this CTA's 64 keys (pages 4X..4X+3 of the tile); the slot frees once QK of tile jj - KS is done
+                    if (jj >= KS && !mbar_wait_warp(&bars->k_empty[st], ((jj / KS) & 1) ^ 1, p.err, abort)) {
+                        ok = false;
+                        break;
+                    }
+                    if (lane == 0 && rank == 0)
+                        mbar_arrive_expect_tx(&bars->k_full[st], npg * SL::kChunks * (JT_PAGE_SIZE * 128));
+                    __syncwarp();
+                    if (lane < npg && (lane >> 2) == static_cast<int>(rank)) {
+                        const uint32_t lead = cluster_map(&bars->k_full[st], 0);
+                        for (int c = 0; c < SL::kChunks; ++c)
+                            tma_load_4d_pair(sK + st * SL::kKHalf + c * SL::kKChunk + (lane & 3) * (JT_PAGE_SIZE * 128),
+                                             &tm_k, lead, c * 64, pc.g, 0, pid);
+                    }
+                }
+            }
+            // on abort the leader lets the copies it counted land before the pair exits
+            if (*abort && rank == 0) {
+                for (int j = max(0, jj - KS); j < jj; ++j)
+                    mbar_wait(&bars->k_full[j % KS], (j / KS) & 1, p.err, nullptr);
+                for (int n = max(0, npc - 2); n < npc; ++n) mbar_wait(&bars->q_full[n & 1], (n >> 1) & 1, p.err, nullptr);
+            }
+        } else if (warp == 10) {
+            // ---------------------------------------------------------- TMA: V
+            Walker w;
+            w.init(p, bars, work);
+            Piece pc;
+            int jj = 0;
+            uint32_t own_seen = 0, own_par = 0;  // per stage: a unit-final copy was issued; phase parity of the last
+            bool ok = true;
+            while (ok && !*abort && w.next(p, pc)) {
+                const int valid_end = unit_end(pc.s, pc.mp, npt);
+                int bt_cur = bt_group(p, pc, valid_end, 0, lane);
+                int bt_nxt = bt_group(p, pc, valid_end, 1, lane);
+                int bt_nn = bt_group(p, pc, valid_end, 2, lane);
+                for (int j = 0; j < pc.nt; ++j, ++jj) {
+                    const int st = jj % VS;
+                    if (j > 0 && (j & 3) == 0) {
+                        bt_cur = bt_nxt;
+                        bt_nxt = bt_nn;
+                        bt_nn = bt_group(p, pc, valid_end, (j >> 2) + 2, lane);
+                    }
+                    const int nvalid = min(kTileN, valid_end - (pc.t0 + j) * kTileN);
+                    const int npg = (nvalid + JT_PAGE_SIZE - 1) / JT_PAGE_SIZE;
+                    const int pid = __shfl_sync(0xFFFFFFFFu, bt_cur, ((j & 3) << 3) + (lane & 7));
+                    // this CTA's D / 2 dims of every key; the slot frees once PV of tile jj - VS is done
+                    if (jj >= VS && !mbar_wait_warp(&bars->v_empty[st], ((jj / VS) & 1) ^ 1, p.err, abort)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t* vt = sV + st * SL::kVHalf;
+                    const int c0 = static_cast<int>(rank) * kHalfCols;
+                    if (pc.t0 + j != pc.T - 1) {
+                        if (lane == 0 && rank == 0)
+                            mbar_arrive_expect_tx(&bars->v_full[st], 2 * npg * (JT_PAGE_SIZE * SL::kVRow));
+                        __syncwarp();
+                        if (lane < npg)
+                            tma_load_4d_pair(vt + lane * (JT_PAGE_SIZE * SL::kVRow), &tm_v,
+                                             cluster_map(&bars->v_full[st], 0), c0, pc.g, 0, pid);
+                    } else {
+                        // a unit's final tile: each CTA lands its half on its own
+                        // barrier; a softmax warp zeroes the rows past the last
+                        // needed slot before it releases the tile's P.  The
+                        // leader's v_full phase of this tile completes empty
+                        if (lane == 0) {
+                            if (rank == 0) mbar_arrive(&bars->v_full[st]);
+                            mbar_arrive_expect_tx(&bars->v_own[st], npg * (JT_PAGE_SIZE * SL::kVRow));
+                        }
+                        __syncwarp();
+                        if (lane < npg)
+                            tma_load_4d(vt + lane * (JT_PAGE_SIZE * SL::kVRow), &tm_v, &bars->v_own[st], c0, pc.g, 0, pid);
+                        own_par = (own_seen >> st & 1u) ? own_par ^ (1u << st) : own_par & ~(1u << st);
+                        own_seen |= 1u << st;
+                    }
+                }
+            }
+            if (*abort) {
+                for (int s = 0; s < VS; ++s)
+                    if (own_seen >> s & 1u) mbar_wait(&bars->v_own[s], own_par >> s & 1u, p.err, nullptr);
+                if (rank == 0)
+                    for (int j = max(0, jj - VS); j < jj; ++j)
+                        mbar_wait(&bars->v_full[j % VS], (j / VS) & 1, p.err, nullptr);
+            }
+        } else if (warp == 9) {
+            // ------------------------------------------------------------ MMA
+            if (rank == 0) {
+                const uint64_t dq0 = smem_desc_sw128(smem_u32(sQ), 16, 1024);
+                const uint64_t dk0 = smem_desc_sw128(smem_u32(sK), 16, 1024);
+                const uint64_t dv0 = v_desc<D>(smem_u32(sV));
+                Walker wq, wv;  // the QKs run up to three tiles ahead of the PVs, across pieces
+                wq.init(p, bars, work);
+                wv.init(p, bars, work);
+                Piece pq;
+                int issued = 0, nq = -1, left_q = 0;  // QKs issued, Q piece, its tiles left
+                bool ok = true;
+                // QK of the next tile; block: wait for its operands, else return
+                // false when they have not landed yet
+                auto qk_next = [&](bool block) -> bool {
+                    if (left_q == 0) {
+                        if (!wq.next(p, pq)) return false;
+                        ++nq;
+                        left_q = -pq.nt;  // negative: the piece's Q has not been waited for
+                    }
+                    const int st = issued % KS;
+                    const uint32_t par = (issued / KS) & 1;
+                    if (block) {
+                        if ((left_q < 0 && !mbar_wait_warp(&bars->q_full[nq & 1], (nq >> 1) & 1, p.err, abort)) ||
+                            !mbar_wait_warp(&bars->k_full[st], par, p.err, abort)) {
+                            ok = false;
+                            return false;
+                        }
+                    } else if ((left_q < 0 &&
+                                !__all_sync(0xFFFFFFFFu, mbar_try_wait(&bars->q_full[nq & 1], (nq >> 1) & 1))) ||
+                               !__all_sync(0xFFFFFFFFu, mbar_try_wait(&bars->k_full[st], par))) {
+                        return false;
+                    }
+                    if (left_q < 0) left_q = -left_q;
+                    tc_fence_after();
+                    issue_qk<D>(tmem + 128 * (issued % 3), dq0 + (nq & 1) * (SL::kQBytes >> 4), dk0 + st * (SL::kKHalf >> 4));
+                    commit_warp(&bars->s_full[issued % 3]);
+                    commit_warp(&bars->k_empty[st]);
+                    if (--left_q == 0) commit_warp(&bars->q_empty[nq & 1]);  // the piece's last QK
+                    ++issued;
+                    return true;
+                };
+                while (ok && issued < min(3, quota)) qk_next(true);
+                Piece pc;
+                int jj = 0, npc = 0;
+                while (ok && wv.next(p, pc)) {
+                    for (int j = 0; ok && j < pc.nt; ++j, ++jj) {
+                        const int st = jj % VS, b = jj % 3;
+                        ok = mbar_wait_warp(&bars->p_full[b], (jj / 3) & 1, p.err, abort) &&
+                             mbar_wait_warp(&bars->v_full[st], (jj / VS) & 1, p.err, abort);
+                        // the previous piece's O has been read out
+                        if (ok && j == 0 && npc > 0) ok = mbar_wait_warp(&bars->o_free, (npc - 1) & 1, p.err, abort);
+                        if (!ok) break;
+                        tc_fence_after();
+                        issue_pv<D>(tmem + 384, tmem + 128 * b, dv0 + st * (SL::kVHalf >> 4), j > 0);
+                        commit_warp(&bars->o_done[b]);
+                        commit_warp(&bars->v_empty[st]);
+                        // S(jj mod 3) is free for QK(jj + 3) once PV(jj) is issued.
+                        // QK(jj + 1) must be on its way before P(jj + 1) is awaited;
+                        // later QKs go now only if their operands have landed, so
+                        // that a late K never holds back the next PV
+                        while (ok && issued < min(jj + 4, quota))
+                            if (!qk_next(issued <= jj + 1)) break;
+                    }
+                    ++npc;
+                }
+                commit_warp(&bars->mma_final);
+            }
+        }
+    } else if (quota > 0) {
+        // ------------------------------------------------------- softmax
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+        const int x = static_cast<int>(rank);
+        const int wg = warp >> 2, w4 = warp & 3;
+        const int r = tid & 127;  // query row = TMEM lane
+        const uint32_t lane_off = static_cast<uint32_t>(w4 * 32) << 16;
+        const uint32_t tO = tmem + 384 + lane_off;
+        const float sl2 = p.scale_log2;
+        uint8_t* stage = smem + SL::kStage + warp * 2048;
+        volatile float* mbuf = reinterpret_cast<volatile float*>(smem + SL::kM);
+        float2* xch = reinterpret_cast<float2*>(smem + SL::kX) + w4 * 128;
+        const uint32_t lead_p = cluster_map(&bars->p_full[0], 0);
+        const uint32_t lead_free = cluster_map(&bars->o_free, 0);
+        Walker w;
+        w.init(p, bars, work);
+        Piece pc;
+        int cnt = 0, npc = 0;               // tiles and pieces so far
+        uint32_t mph = 0, own_seen = 0, own_par = 0;  // m_bar phase parities per tile parity; v_own phases
+        int xph = 0;
+        auto meet8 = [&](int i) -> bool {   // meeting i of a merge (a merge meets twice: parity i)
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->msync);
+            return mbar_wait_warp(&bars->msync, static_cast<uint32_t>(i), p.err, abort);
+        };
+        bool ok = true;
+        while (ok && w.next(p, pc)) {
+            const bool tile_on = (2 * pc.mp + x) * npt < pc.s.B;  // this CTA's query tile exists
+            const int L = pc.s.L;
+            const int tok0 = (2 * pc.mp + x) * npt;
+            const int token = tok0 + r / p.G;
+            const int head = pc.g * p.G + r % p.G;
+            const bool valid_row = r < npt * p.G && token < pc.s.B;
+            const bool warp_on = __any_sync(0xFFFFFFFFu, valid_row);
+            const int first_masked = L + tok0 + 1;  // tiles that end before this slot need no mask
+            float m_run = -INFINITY, l_run = 0.0f;
+            for (int j = 0; j < pc.nt; ++j, ++cnt) {
+                const int b = cnt % 3;
+                const bool mine = (cnt & 1) == wg;
+                if (!mine && warp_on) {
+                    mph ^= 1u << (cnt & 1);  // the other warpgroup's tile: one more phase of its m_bar
+                    continue;
+                }
+                if (!mbar_wait_warp(&bars->s_full[b], (cnt / 3) & 1, p.err, abort)) {
+                    ok = false;
+                    break;
+                }
+                if (!mine) continue;
+                tc_fence_after();
+                if (warp_on) {
+                    const uint32_t tS = tmem + 128 * b + lane_off;
+                    const int slot0 = (pc.t0 + j) * kTileN;
+                    SRow sr;
+                    load_srow(tS, sr);
+                    if (slot0 + kTileN > first_masked) mask_srow(sr, L + token + 1 - slot0);
+                    const float mx_s = max_srow(sr) * sl2;
+                    // the row's maximum after the tile before, from the partner warp
+                    float m_prev = -INFINITY;
+                    if (j > 0) {
+                        const int o = (cnt - 1) & 1;
+                        if (!mbar_wait_warp(&bars->m_bar[w4][o], ((mph >> o) & 1u) ^ 1u, p.err, abort)) {
+                            ok = false;
+                            break;
+                        }
+                        m_prev = mbuf[o * 128 + r];
+                    }
+                    float m_new = m_prev, factor = 1.0f;
+                    bool resc = false;
+                    if (mx_s > m_prev + kRescaleLog2 || m_prev == -INFINITY) {
+                        m_new = fmaxf(m_prev, mx_s);
+                        resc = m_prev != -INFINITY && valid_row;
+                        if (resc) factor = ex2_approx(m_prev - m_new);
+                    }
+                    mbuf[(cnt & 1) * 128 + r] = m_new;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars->m_bar[w4][cnt & 1]);
+                    mph ^= 1u << (cnt & 1);
+                    if (m_new != m_run) {  // this warp's part of the sum follows
+                        l_run = m_run == -INFINITY ? 0.0f : l_run * ex2_approx(m_run - m_new);
+                        m_run = m_new;
+                    }
+                    // P = exp2(s*scale*log2e - m), written over S (bf16 pairs)
+                    l_run += exp_store_srow(sr, tS, sl2, m_run == -INFINITY ? 0.0f : m_run);
+                    if (__any_sync(0xFFFFFFFFu, resc)) {
+                        // O holds PV(cnt - 1) before it is rescaled
+                        if (!mbar_wait_warp(&bars->o_done[(cnt - 1) % 3], ((cnt - 1) / 3) & 1, p.err, abort)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int q = 0; q < D / 32; ++q) {
+                            uint32_t v[32];
+                            tmem_ld32(tO + q * 32, v);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) * factor);
+                            tmem_st32(tO + q * 32, v);
+                        }
+                    }
+                    tmem_wait_st();
+                }
+                if (pc.t0 + j == pc.T - 1 && w4 == 0) {
+                    // the unit's final tile: zero the rows of its last page past the last needed slot
+                    const int st = cnt % VS;
+                    const uint32_t par = (own_seen >> st & 1u) ? (own_par >> st & 1u) ^ 1u : 0u;
+                    if (!mbar_wait_warp(&bars->v_own[st], par, p.err, abort)) {
+                        ok = false;
+                        break;
+                    }
+                    const int nvalid = unit_end(pc.s, pc.mp, npt) - (pc.t0 + j) * kTileN;
+                    const int end = (nvalid + JT_PAGE_SIZE - 1) / JT_PAGE_SIZE * JT_PAGE_SIZE;
+                    for (int i = lane; i < (end - nvalid) * (SL::kVRow / 16); i += 32)
+                        reinterpret_cast<uint4*>(sV + st * SL::kVHalf + nvalid * SL::kVRow)[i] = make_uint4(0u, 0u, 0u, 0u);
+                    fence_proxy_async_smem();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(lead_p + 8 * b);
+            }
+            if (!ok) break;
+            if (pc.t0 + pc.nt == pc.T) {  // the unit's final tile used one more phase of its v_own
+                const int st = (cnt - 1) % VS;
+                own_par = (own_seen >> st & 1u) ? own_par ^ (1u << st) : own_par & ~(1u << st);
+                own_seen |= 1u << st;
+            }
+            if (w.remaining <= 0) pdl_trigger();
+            // ------------------------------------------- end of the piece
+            float m_tot = -INFINITY, l_tot = 0.0f;
+            if (warp_on) {
+                // both warps of the rows: whole maxima and sums
+                float2* xp = xch + (npc & 1) * 64;
+                xp[wg * 32 + lane] = make_float2(m_run, l_run);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars->x_bar[w4]);
+                if (!mbar_wait_warp(&bars->x_bar[w4], xph & 1, p.err, abort)) {
+                    ok = false;
+                    break;
+                }
+                ++xph;
+                const float2 a = xp[lane], c = xp[32 + lane];  // in this order for both warps
+                m_tot = fmaxf(a.x, c.x);
+                const float fa = a.x == -INFINITY ? 0.0f : ex2_approx(a.x - m_tot);
+                const float fc = c.x == -INFINITY ? 0.0f : ex2_approx(c.x - m_tot);
+                l_tot = a.y * fa + c.y * fc;
+            }
+            ++npc;
+            if (!mbar_wait_warp(&bars->o_done[(cnt - 1) % 3], ((cnt - 1) / 3) & 1, p.err, abort)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const bool partial = pc.slot >= 0;
+            uint32_t v[kHalfCols / 32][32];
+            if (warp_on) {
+#pragma unroll
+                for (int h = 0; h < kHalfCols / 32; ++h) tmem_ld32(tO + wg * kHalfCols + 32 * h, v[h]);
+                tmem_wait_ld();
+            }
+            // O has been read: the next piece's first PV may overwrite it
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(lead_free);
+            const long long rowid = static_cast<long long>(pc.s.off + token) * p.Hq + head;
+            if (warp_on && partial) {
+                const long long prow = (static_cast<long long>(pc.slot) * 2 + x) * kTileM + r;
+#pragma unroll
+                for (int h = 0; h < kHalfCols / 32; ++h) {
+                    uint4 slot[8];
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+                        slot[c] = make_uint4(v[h][4 * c], v[h][4 * c + 1], v[h][4 * c + 2], v[h][4 * c + 3]);
+                    const int col = wg * kHalfCols + 32 * h;
+                    float* base = p.part_o + prow * D + col;
+                    if (valid_row)
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) reinterpret_cast<uint4*>(base)[c] = slot[c];
+                }
+                if (wg == 0 && valid_row) p.part_ml[prow] = make_float2(m_tot, l_tot);
+            } else if (warp_on) {
+                const float inv = 1.0f / l_tot;
+                float probe = 0.0f;
+#pragma unroll
+                for (int h = 0; h < kHalfCols / 32; ++h) {
+                    uint4 slot[4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        float o[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            o[i] = __uint_as_float(v[h][8 * c + i]) * inv;
+                            probe += o[i] * 0.0f;
+                        }
+                        slot[c] = make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]),
+                                             pack_bf16x2(o[6], o[7]));
+                    }
+                    const int col = wg * kHalfCols + 32 * h;
+                    stage_store<4>(stage, lane, slot, [&](int rr) {
+                        const long long rid = __shfl_sync(0xFFFFFFFFu, rowid, rr);
+                        const bool rvalid = __shfl_sync(0xFFFFFFFFu, valid_row, rr);
+                        return rvalid ? reinterpret_cast<uint4*>(p.out + rid * D + col) : nullptr;
+                    });
+                }
+                if (wg == 0 && valid_row && p.lse) p.lse[rowid] = (m_tot + log2f(l_tot)) * 0.6931471805599453f;
+                unsigned bad = __ballot_sync(0xFFFFFFFFu, valid_row && probe != 0.0f && l_tot == l_tot);
+                while (bad) {
+                    const int rr = __ffs(bad) - 1;
+                    bad &= bad - 1;
+                    __syncwarp();
+                    redo_row<D, kHalfCols / 32>(p, pc.b, L, pc.g, __shfl_sync(0xFFFFFFFFu, token, rr),
+                                                __shfl_sync(0xFFFFFFFFu, rowid, rr), wg * kHalfCols, lane);
+                }
+            }
+            if (partial && tile_on) {
+                // count this piece done; the slot that completes the unit merges every piece's rows
+                const CutUnit cu(pc.gpos - pc.t0, pc.T, bars->w_P);
+                __threadfence();  // this thread's partial rows are visible GPU-wide
+                if (!meet8(0)) {
+                    ok = false;
+                    break;
+                }
+                if (tid == 0) {
+                    const uint32_t cid = bars->call_id;
+                    unsigned long long* ctr = p.merge_cnt + 2 * cu.c0 + x;
+                    unsigned long long old = *reinterpret_cast<volatile unsigned long long*>(ctr), assumed, nv;
+                    do {  // a count from an earlier call restarts at this call's first piece
+                        assumed = old;
+                        nv = ((assumed >> 32) == cid) ? assumed + 1ull
+                                                      : ((static_cast<unsigned long long>(cid) << 32) | 1ull);
+                        old = atomicCAS(ctr, assumed, nv);
+                    } while (old != assumed);
+                    bars->merge_flag = static_cast<int>(nv & 0xFFFFFFFFull) == cu.n;
+                    __threadfence();  // the other pieces' rows are read after this count
+                }
+                if (!meet8(1)) {
+                    ok = false;
+                    break;
+                }
+                if (bars->merge_flag) merge_rows<D>(p, pc, cu, x, warp, lane);
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    // both CTAs: every MMA of the pair has completed before TMEM is released
+    if (warp == 9 && quota > 0) mbar_wait_warp(&bars->mma_final, 0, p.err, nullptr);
+    cluster_sync();  // no copy, arrive or MMA of the pair targets either CTA any more
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, 512);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+typedef CUresult (*PFN_encodeTiled_t)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                      const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                      CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+static PFN_encodeTiled_t encode_fn() {
+    static const PFN_encodeTiled_t fn = [] {
+        void* ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        const bool got = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault,
+                                                          &q) == cudaSuccess &&
+                         q == cudaDriverEntryPointSuccess;
+        return got ? reinterpret_cast<PFN_encodeTiled_t>(ptr) : nullptr;
+    }();
+    return fn;
+}
+
+// The merge counts sit between the header and a fixed offset, whatever the
+// head dim and dtype of the calls that share a workspace.
+constexpr int kMaxSlots = static_cast<int>((kChunkFixedBytes - kWsHeader) / 16);
+
+// Work slots on the current device: the clusters of two CTAs that can be
+// resident at once (one CTA per SM).
+template <int D>
+static int work_slots() {
+    static PerDeviceCache cache;
+    const int n = cache.get([] {
+        const int fallback = std::max(1, device_sm_count() / 2);
+        if (cudaFuncSetAttribute(chunk_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kAlloc) !=
+            cudaSuccess) {
+            (void)cudaGetLastError();
+            return fallback;
+        }
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(2 * fallback);
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = Smem<D>::kAlloc;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 2;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, chunk_attn_kernel<D>, &cfg) != cudaSuccess || n < 1) {
+            (void)cudaGetLastError();
+            return fallback;
+        }
+        return n;
+    });
+    return std::min(n, kMaxSlots);
+}
+
+static size_t ml_bytes(int slots) { return align_up(static_cast<size_t>(2) * slots * 2 * kTileM * sizeof(float2)); }
+
+template <int D>
+static cudaError_t launch(const ChunkArgs& a, char* ws, cudaStream_t st) {
+    PFN_encodeTiled_t enc = encode_fn();
+    if (!enc) return cudaErrorNotSupported;
+    const int slots = work_slots<D>();
+    const int G = a.Hq / a.Hkv, npt = kTileM / G;
+    const cuuint64_t eD = D, eHq = a.Hq, eHkv = a.Hkv;
+    const cuuint32_t es[4] = {1, 1, 1, 1};
+    CUtensorMap tq, tk, tv;
+    {
+        const cuuint64_t dims[3] = {eD, eHq, static_cast<cuuint64_t>(a.total)};
+        const cuuint64_t strides[2] = {eD * 2, eHq * eD * 2};
+        const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(G), static_cast<cuuint32_t>(npt)};
+        if (enc(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(a.q), dims, strides, box, es,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return cudaErrorInvalidValue;
+    }
+    {
+        const cuuint64_t dims[4] = {eD, eHkv, JT_PAGE_SIZE, static_cast<cuuint64_t>(a.num_pages)};
+        const cuuint64_t strides[3] = {eD * 2, eHkv * eD * 2, JT_PAGE_SIZE * eHkv * eD * 2};
+        const cuuint32_t kbox[4] = {64, 1, JT_PAGE_SIZE, 1};
+        const cuuint32_t vbox[4] = {D / 2, 1, JT_PAGE_SIZE, 1};
+        if (enc(&tk, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(a.k_cache), dims, strides, kbox, es,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS ||
+            enc(&tv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(a.v_cache), dims, strides, vbox, es,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return cudaErrorInvalidValue;
+    }
+    Params prm;
+    prm.block_table = a.block_table;
+    prm.prefix_len = a.prefix_len;
+    prm.off = a.chunk_off;
+    prm.q = static_cast<const __nv_bfloat16*>(a.q);
+    prm.k_cache = static_cast<const __nv_bfloat16*>(a.k_cache);
+    prm.v_cache = static_cast<const __nv_bfloat16*>(a.v_cache);
+    prm.out = static_cast<__nv_bfloat16*>(a.out);
+    prm.lse = a.lse;
+    char* w = ws + kWsHeader;
+    prm.merge_cnt = reinterpret_cast<unsigned long long*>(w);
+    w += kChunkFixedBytes - kWsHeader;
+    prm.part_ml = reinterpret_cast<float2*>(w);
+    w += ml_bytes(slots);
+    prm.part_o = reinterpret_cast<float*>(w);
+    prm.tickets = &reinterpret_cast<WsHeader*>(ws)->tickets;
+    prm.err = reinterpret_cast<uint32_t*>(ws);
+    prm.max_pages = a.max_pages;
+    prm.num_pages = a.num_pages;
+    prm.nseq = a.nseq;
+    prm.total = a.total;
+    prm.max_chunk = a.max_chunk;
+    prm.Hq = a.Hq;
+    prm.Hkv = a.Hkv;
+    prm.G = G;
+    prm.npt = npt;
+    prm.scale_log2 = a.scale * 1.4426950408889634f;
+    static PerDeviceCache attr;  // the shared-memory opt-in is per device
+    const cudaError_t ea = static_cast<cudaError_t>(attr.get([] {
+        return static_cast<int>(cudaFuncSetAttribute(chunk_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                     Smem<D>::kAlloc));
+    }));
+    if (ea != cudaSuccess) return ea;
+    return launch_kernel_pdl(chunk_attn_kernel<D>, dim3(2 * slots), dim3(kThreads), Smem<D>::kAlloc, st, tq, tk, tv,
+                             prm);
+}
+
+}  // namespace chunk
+
+size_t chunk_attn_bf16_workspace_bytes(int D) {
+    if (D != 64 && D != 128) return kChunkFixedBytes;
+    const int slots = D == 128 ? chunk::work_slots<128>() : chunk::work_slots<64>();
+    return kChunkFixedBytes + chunk::ml_bytes(slots) +
+           align_up(static_cast<size_t>(2) * slots * 2 * chunk::kTileM * D * sizeof(float));
+}
+
+cudaError_t chunk_attn_bf16_launch(const ChunkArgs& a, char* ws, cudaStream_t st) {
+    if (a.D == 128) return chunk::launch<128>(a, ws, st);
+    if (a.D == 64) return chunk::launch<64>(a, ws, st);
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace jt

@@ -3,6 +3,8 @@
 #include <math.h>
 #include <string.h>
 
+#include <algorithm>
+
 #include "jt_common.cuh"
 #include "jt_internal.h"
 
@@ -45,7 +47,7 @@ using namespace jt;
 
 extern "C" {
 
-int jt_version(void) { return 1 * 10000 + 0 * 100 + 0; }
+int jt_version(void) { return 1 * 10000 + 1 * 100 + 0; }
 
 const char* jt_status_str(jt_status s) {
     switch (s) {
@@ -80,7 +82,14 @@ size_t jt_workspace_size(int op, int nseq, int N, int W, int64_t V, int total_no
             if (nseq < 1 || total_nodes < 1) return 0;
             return accept_workspace_bytes(nseq, total_nodes);
         case JT_OP_TREE_POLICY:
+        case JT_OP_QKV_APPEND:
             return kWsHeader;
+        case JT_OP_CHUNK_ATTN:
+            if (nseq < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || D < 1 || max_pages < 1 || max_tree < 1) return 0;
+            return std::max(chunk_attn_bf16_workspace_bytes(D),
+                            chunk_attn_f32_workspace_bytes(nseq, Hq, Hkv, D, max_pages, max_tree));
+        case JT_OP_KV_COMMIT:
+            return nseq < 1 ? 0 : kv_commit_workspace_bytes(nseq);
         default:
             return 0;
     }
@@ -291,6 +300,153 @@ jt_status jt_verify_accept_stochastic(const float* target_logits, const float* d
     return from_cuda(verify_stochastic_launch(target_logits, draft_logits, parent, token, tree_off, nseq, N, V,
                                               total_nodes, u_accept, u_bonus, accept_len, path, bonus,
                                               static_cast<char*>(ws), stream));
+}
+
+jt_status jt_qkv_append(const void* qkv, int dtype, int64_t row_stride, const void* q_weight,
+                        const void* k_weight, float eps, const float* cos_sin, int max_pos,
+                        int rot_dim, int interleaved, const int32_t* depth,
+                        const int32_t* block_table, int max_pages, int num_pages,
+                        const int32_t* prefix_len, const int32_t* tree_off, int nseq,
+                        int total_nodes, int Hq, int Hkv, int D, int page_size, void* q_out,
+                        void* k_cache, void* v_cache, void* ws, size_t ws_bytes,
+                        jt_stream_t stream) {
+    JT_RANGE("jt_qkv_append");
+    if (total_nodes < 0 || nseq < 1 || nseq > 65535 || Hq < 0 || Hkv < 1 || D < 1 || max_pages < 1 ||
+        num_pages < 1 || page_size != JT_PAGE_SIZE || rot_dim < 0 || rot_dim > D ||
+        (interleaved != 0 && interleaved != 1) || !(eps >= 0.0f) || !isfinite(eps) ||
+        (dtype != JT_DTYPE_BF16 && dtype != JT_DTYPE_F32))
+        return JT_ERR_INVALID;
+    const bool bf16 = dtype == JT_DTYPE_BF16;
+    if (bf16 ? (D != 64 && D != 128) : (D != 32 && D != 64 && D != 96 && D != 128)) return JT_ERR_UNSUPPORTED;
+    if (rot_dim % (bf16 ? 16 : 8) != 0) return JT_ERR_UNSUPPORTED;
+    if (total_nodes == 0) return JT_OK;
+    if (!qkv || !block_table || !prefix_len || !tree_off || !k_cache || !v_cache || (Hq > 0 && !q_out) ||
+        (rot_dim > 0 && (!cos_sin || max_pos < 1)) ||
+        row_stride < (static_cast<int64_t>(Hq) + 2 * static_cast<int64_t>(Hkv)) * D || row_stride % (bf16 ? 8 : 4) != 0)
+        return JT_ERR_INVALID;
+    if (!aligned(qkv, 16) || !aligned(q_weight, 16) || !aligned(k_weight, 16) || !aligned(cos_sin, 16) ||
+        !aligned(q_out, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16))
+        return JT_ERR_INVALID;
+    jt_status s = check_ws(ws, ws_bytes, kWsHeader);
+    if (s != JT_OK) return s;
+    AppendArgs a;
+    a.qkv = qkv;
+    a.q_weight = q_weight;
+    a.k_weight = k_weight;
+    a.cos_sin = cos_sin;
+    a.depth = depth;
+    a.block_table = block_table;
+    a.prefix_len = prefix_len;
+    a.tree_off = tree_off;
+    a.q_out = q_out;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.row_stride = row_stride;
+    a.dtype = dtype;
+    a.max_pos = max_pos;
+    a.rot_dim = rot_dim;
+    a.interleaved = interleaved;
+    a.max_pages = max_pages;
+    a.num_pages = num_pages;
+    a.nseq = nseq;
+    a.total = total_nodes;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.D = D;
+    a.eps = eps;
+    return from_cuda(qkv_append_launch(a, static_cast<uint32_t*>(ws), stream));
+}
+
+jt_status jt_chunk_attn_paged(const void* q, const void* k_cache, const void* v_cache, int dtype,
+                              const int32_t* block_table, int max_pages, int num_pages,
+                              const int32_t* prefix_len, const int32_t* chunk_off, int nseq,
+                              int total_tokens, int max_chunk, int Hq, int Hkv, int D,
+                              int page_size, float scale, void* out, float* lse, void* ws,
+                              size_t ws_bytes, jt_stream_t stream) {
+    JT_RANGE("jt_chunk_attn_paged");
+    if (total_tokens < 0 || nseq < 1 || nseq > 65535 || max_chunk < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 ||
+        D < 1 || max_pages < 1 || num_pages < 1 || page_size != JT_PAGE_SIZE || !isfinite(scale) ||
+        (dtype != JT_DTYPE_BF16 && dtype != JT_DTYPE_F32))
+        return JT_ERR_INVALID;
+    const bool bf16 = dtype == JT_DTYPE_BF16;
+    const int G = Hq / Hkv;
+    if (bf16 ? (D != 64 && D != 128) : (D != 32 && D != 64 && D != 96 && D != 128)) return JT_ERR_UNSUPPORTED;
+    if (G > (bf16 ? 128 : 64)) return JT_ERR_UNSUPPORTED;
+    if (!bf16 && static_cast<long long>(nseq) * Hkv * ((static_cast<long long>(max_chunk) + 64 / G - 1) / (64 / G)) >
+                     0x7FFFFFFFll)
+        return JT_ERR_UNSUPPORTED;
+    if (total_tokens == 0) return JT_OK;
+    if (!q || !k_cache || !v_cache || !block_table || !prefix_len || !chunk_off || !out || !aligned(q, 16) ||
+        !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16))
+        return JT_ERR_INVALID;
+    jt_status s = check_ws(ws, ws_bytes,
+                           bf16 ? chunk_attn_bf16_workspace_bytes(D)
+                                : chunk_attn_f32_workspace_bytes(nseq, Hq, Hkv, D, max_pages, max_chunk));
+    if (s != JT_OK) return s;
+    ChunkArgs a;
+    a.q = q;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.block_table = block_table;
+    a.prefix_len = prefix_len;
+    a.chunk_off = chunk_off;
+    a.max_pages = max_pages;
+    a.num_pages = num_pages;
+    a.nseq = nseq;
+    a.total = total_tokens;
+    a.max_chunk = max_chunk;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.D = D;
+    a.scale = scale;
+    a.out = out;
+    a.lse = lse;
+    char* base = static_cast<char*>(ws);
+    return from_cuda(bf16 ? chunk_attn_bf16_launch(a, base, stream) : chunk_attn_f32_launch(a, base, stream));
+}
+
+jt_status jt_kv_commit(void* k_cache, void* v_cache, int dtype, int layers, int64_t layer_stride,
+                       const int32_t* block_table, int max_pages, int num_pages,
+                       const int32_t* prefix_len, const int32_t* tree_off,
+                       const int32_t* accept_len, const int32_t* path, int nseq, int N, int Hkv,
+                       int D, int page_size, int32_t* new_prefix, void* ws, size_t ws_bytes,
+                       jt_stream_t stream) {
+    JT_RANGE("jt_kv_commit");
+    if (!k_cache || !v_cache || !block_table || !prefix_len || !tree_off || !accept_len || !path || !new_prefix ||
+        nseq < 1 || nseq > 65535 || N < 0 || N > JT_MAX_TREE || layers < 1 || layers > 65535 || max_pages < 1 ||
+        num_pages < 1 || Hkv < 1 || D < 1 || page_size != JT_PAGE_SIZE ||
+        (dtype != JT_DTYPE_BF16 && dtype != JT_DTYPE_F32))
+        return JT_ERR_INVALID;
+    const int64_t esize = dtype == JT_DTYPE_BF16 ? 2 : 4;
+    const int64_t row = static_cast<int64_t>(Hkv) * D * esize;
+    if (row % 16 != 0 || row > (1 << 24)) return JT_ERR_UNSUPPORTED;
+    if (layers > 1 && (layer_stride < static_cast<int64_t>(num_pages) * JT_PAGE_SIZE * Hkv * D ||
+                       layer_stride * esize % 16 != 0))
+        return JT_ERR_INVALID;
+    if (!aligned(k_cache, 16) || !aligned(v_cache, 16)) return JT_ERR_INVALID;
+    const uintptr_t x = reinterpret_cast<uintptr_t>(new_prefix), y = reinterpret_cast<uintptr_t>(prefix_len);
+    const uintptr_t n = static_cast<uintptr_t>(nseq) * sizeof(int32_t);
+    const bool in_place = x == y;
+    if (!in_place && x < y + n && y < x + n) return JT_ERR_INVALID;  // partly overlapping
+    jt_status s = check_ws(ws, ws_bytes, in_place ? kv_commit_workspace_bytes(nseq) : kWsHeader);
+    if (s != JT_OK) return s;
+    CommitArgs a;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.block_table = block_table;
+    a.prefix_len = prefix_len;
+    a.tree_off = tree_off;
+    a.accept_len = accept_len;
+    a.path = path;
+    a.new_prefix = new_prefix;
+    a.layer_stride = layers > 1 ? layer_stride * esize : 0;
+    a.row_bytes = static_cast<int>(row);
+    a.layers = layers;
+    a.max_pages = max_pages;
+    a.num_pages = num_pages;
+    a.nseq = nseq;
+    a.N = N;
+    return from_cuda(kv_commit_launch(a, static_cast<char*>(ws), stream));
 }
 
 jt_status jt_check(void* ws, jt_stream_t stream) {

@@ -36,7 +36,7 @@ inline size_t align_up(size_t n) { return (n + kAlign - 1) / kAlign * kAlign; }
 // Workspace header (first kAlign bytes of every workspace).
 struct WsHeader {
     uint32_t err;                // device error flags (DEVERR_*)
-    uint32_t reserved;
+    uint32_t arrivals;           // kv_commit: CTAs of the running call that have read their lengths (0 between calls)
     unsigned long long tickets;  // attention: CTA arrivals over all calls (call number = tickets / grid)
 };
 constexpr size_t kWsHeader = kAlign;
@@ -104,6 +104,60 @@ cudaError_t tree_attn_f32_launch(const float* q, const float* k_cache, const flo
                                  const uint32_t* anc, int nseq, int total_nodes, int Hq, int Hkv,
                                  int D, float scale, float* out, float* lse, uint32_t* err,
                                  cudaStream_t st);
+
+// chunk_attn.cu / chunk_attn_f32.cu
+struct ChunkArgs {
+    const void* q;
+    const void* k_cache;
+    const void* v_cache;
+    const int32_t* block_table;
+    const int32_t* prefix_len;
+    const int32_t* chunk_off;
+    int max_pages, num_pages, nseq, total, max_chunk, Hq, Hkv, D;
+    float scale;
+    void* out;
+    float* lse;
+};
+// header and merge counts: zero before a workspace's first use
+constexpr size_t kChunkFixedBytes = 4096;
+// whole workspace (header included) of a call on the current device
+size_t chunk_attn_bf16_workspace_bytes(int D);
+size_t chunk_attn_f32_workspace_bytes(int nseq, int Hq, int Hkv, int D, int max_pages, int max_chunk);
+cudaError_t chunk_attn_bf16_launch(const ChunkArgs& a, char* ws, cudaStream_t st);
+cudaError_t chunk_attn_f32_launch(const ChunkArgs& a, char* ws, cudaStream_t st);
+
+// kv_cache.cu
+struct AppendArgs {
+    const void* qkv;
+    const void* q_weight;
+    const void* k_weight;
+    const float* cos_sin;
+    const int32_t* depth;
+    const int32_t* block_table;
+    const int32_t* prefix_len;
+    const int32_t* tree_off;
+    void* q_out;
+    void* k_cache;
+    void* v_cache;
+    long long row_stride;  // elements
+    int dtype, max_pos, rot_dim, interleaved, max_pages, num_pages, nseq, total, Hq, Hkv, D;
+    float eps;
+};
+cudaError_t qkv_append_launch(const AppendArgs& a, uint32_t* err, cudaStream_t st);
+struct CommitArgs {
+    void* k_cache;
+    void* v_cache;
+    const int32_t* block_table;
+    const int32_t* prefix_len;
+    const int32_t* tree_off;
+    const int32_t* accept_len;
+    const int32_t* path;
+    int32_t* new_prefix;
+    long long layer_stride;  // bytes
+    int row_bytes, layers, max_pages, num_pages, nseq, N;
+};
+size_t kv_commit_workspace_bytes(int nseq);
+cudaError_t kv_commit_launch(const CommitArgs& a, char* ws, cudaStream_t st);
 
 // jt_selftest.cu
 cudaError_t selftest_wait_timeout_launch(uint32_t* err, cudaStream_t st);

@@ -1,0 +1,400 @@
+// kv_cache.cu -- the writers of the paged KV cache: new tokens' keys and values
+// (with the per-head norm and the position rotation on the way), and the move
+// of an accepted path's keys and values behind the prefix.
+#include <algorithm>
+
+#include "jt_common.cuh"
+#include "jt_internal.h"
+
+namespace jt {
+namespace kv {
+
+// ---------------------------------------------------------------------------
+// qkv_append: per token i of sequence b and head h of the packed projection
+//     y = x * rsqrt(mean(x^2) + eps) * w         (q and k heads, with weights)
+//     (a, b) -> (a cos - b sin, b cos + a sin)   (q and k heads, rotated pairs)
+// fp32 throughout, one rounding; q goes to q_out, k and v to slot L_b + i.
+//
+// A head vector is shared by LPH lanes; a lane holds kPairs rotation pairs, as
+// two 16-byte vectors: elements (j, j + rot/2) of the half-split layout or (2j,
+// 2j + 1) of the interleaved one, and the plain rest in order.  So the rotation
+// needs no exchange between lanes and the norm one sum over LPH.  A warp stays
+// with one token: its angles sit in registers for all heads, four heads' loads
+// are in flight per lane.  Bound: HBM bytes (one read, one write of every
+// element) for many tokens, a chain of dependent loads (offsets, prefix, page,
+// row) for one.
+// ---------------------------------------------------------------------------
+struct Append {
+    const void* qkv;
+    const void* q_weight;
+    const void* k_weight;
+    const float* cos_sin;
+    const int32_t* depth;
+    const int32_t* block_table;
+    const int32_t* prefix_len;
+    const int32_t* off;
+    void* q_out;
+    void* k_cache;
+    void* v_cache;
+    uint32_t* err;
+    long long row_stride;
+    int max_pos, rot, interleaved, max_pages, num_pages, nseq, total, Hq, Hkv, warps_per_token;
+    float eps;
+};
+
+template <typename T>
+struct Vec;  // 16 bytes as floats
+template <>
+struct Vec<float> {
+    static constexpr int N = 4;
+    static __device__ __forceinline__ void unpack(const uint4& u, float (&f)[4]) {
+        f[0] = __uint_as_float(u.x), f[1] = __uint_as_float(u.y), f[2] = __uint_as_float(u.z), f[3] = __uint_as_float(u.w);
+    }
+    static __device__ __forceinline__ uint4 pack(const float (&f)[4]) {
+        return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+    }
+};
+template <>
+struct Vec<__nv_bfloat16> {
+    static constexpr int N = 8;
+    static __device__ __forceinline__ void unpack(const uint4& u, float (&f)[8]) {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = __uint_as_float(w[i] << 16);
+            f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+    }
+    static __device__ __forceinline__ uint4 pack(const float (&f)[8]) {
+        return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                          pack_bf16x2(f[6], f[7]));
+    }
+};
+
+// The last sequence whose offset is at most i (one warp; a few steps of 32).
+__device__ __forceinline__ int find_seq(const int32_t* off, int nseq, int i, int lane) {
+    int lo = 0, n = nseq;
+    while (n > 1) {
+        const int step = (n + 31) / 32;
+        const bool le = lane * step < n && off[lo + lane * step] <= i;
+        const int k = 31 - __clz(__ballot_sync(0xFFFFFFFFu, le) | 1u);
+        lo += k * step;
+        n = min(step, n - k * step);
+    }
+    return lo;
+}
+
+constexpr int kAppendThreads = 128;
+constexpr int kUnroll = 4;  // heads in flight per lane group
+
+template <typename T, int D, int LPH>
+__global__ void __launch_bounds__(kAppendThreads) qkv_append_kernel(const Append p) {
+    constexpr int N = Vec<T>::N;              // pairs per lane
+    constexpr int kActive = D / 2 / N;        // lanes of a head that hold elements
+    constexpr int kHeads = 32 / LPH;          // heads per warp at a time
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & 31;
+    const long long gw = static_cast<long long>(blockIdx.x) * (kAppendThreads / 32) + (threadIdx.x >> 5);
+    const int i = static_cast<int>(gw / p.warps_per_token), part = static_cast<int>(gw % p.warps_per_token);
+    if (i >= p.total || i >= p.off[p.nseq]) return;
+    const int b = find_seq(p.off, p.nseq, i, lane);
+    const int o = p.off[b], B = p.off[b + 1] - o, L = p.prefix_len[b], local = i - o;
+    const long long slot = static_cast<long long>(L) + local;
+    const int step = p.depth ? p.depth[i] : local;
+    const long long pos = static_cast<long long>(L) + step;
+    bool ok = o >= 0 && local >= 0 && local < B && o <= p.total - B && L >= 0 &&
+              static_cast<long long>(L) + B <= static_cast<long long>(p.max_pages) * JT_PAGE_SIZE &&
+              (p.rot == 0 || (step >= 0 && pos < p.max_pos));
+    int page = 0;
+    if (ok) {
+        page = p.block_table[static_cast<long long>(b) * p.max_pages + slot / JT_PAGE_SIZE];
+        ok = page >= 0 && page < p.num_pages;
+    }
+    if (!ok) {
+        if (lane == 0) raise_error(p.err, DEVERR_INVALID);
+        return;
+    }
+    const int t = lane % LPH;
+    const bool on = kActive == LPH || t < kActive;
+    const int p0 = t * N;  // first of this lane's pairs
+    const bool rotated = on && p0 < p.rot / 2;
+    const bool split = rotated && !p.interleaved;
+    const int e0 = on ? (split ? p0 : 2 * p0) : 0, e1 = on ? (split ? p.rot / 2 + p0 : 2 * p0 + N) : 0;
+    float cs[N], sn[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) cs[j] = 1.0f, sn[j] = 0.0f;
+    if (rotated) {
+        const float* tab = p.cos_sin + pos * p.rot + p0;
+#pragma unroll
+        for (int j = 0; j < N; j += 4) {
+            const float4 c = *reinterpret_cast<const float4*>(tab + j);
+            const float4 s = *reinterpret_cast<const float4*>(tab + p.rot / 2 + j);
+            cs[j] = c.x, cs[j + 1] = c.y, cs[j + 2] = c.z, cs[j + 3] = c.w;
+            sn[j] = s.x, sn[j + 1] = s.y, sn[j + 2] = s.z, sn[j + 3] = s.w;
+        }
+    }
+    const T* row = static_cast<const T*>(p.qkv) + i * p.row_stride;
+    const int H = p.Hq + 2 * p.Hkv;
+    const long long cache_row = (static_cast<long long>(page) * JT_PAGE_SIZE + slot % JT_PAGE_SIZE) * p.Hkv;
+    for (int h0 = part * kHeads + lane / LPH; __any_sync(0xFFFFFFFFu, h0 < H);
+         h0 += p.warps_per_token * kHeads * kUnroll) {
+        uint4 va[kUnroll], vb[kUnroll];
+#pragma unroll
+        for (int q = 0; q < kUnroll; ++q) {
+            const int h = h0 + q * p.warps_per_token * kHeads;
+            va[q] = vb[q] = make_uint4(0u, 0u, 0u, 0u);
+            if (on && h < H) {
+                va[q] = *reinterpret_cast<const uint4*>(row + static_cast<long long>(h) * D + e0);
+                vb[q] = *reinterpret_cast<const uint4*>(row + static_cast<long long>(h) * D + e1);
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < kUnroll; ++q) {
+            const int h = h0 + q * p.warps_per_token * kHeads;
+            if (!__any_sync(0xFFFFFFFFu, h < H)) break;
+            const bool is_q = h < p.Hq, is_v = h >= p.Hq + p.Hkv;
+            const T* wt = static_cast<const T*>(is_q ? p.q_weight : p.k_weight);
+            float fa[N], fb[N];
+            Vec<T>::unpack(va[q], fa);
+            Vec<T>::unpack(vb[q], fb);
+            float ss = 0.0f;
+#pragma unroll
+            for (int j = 0; j < N; ++j) ss = fmaf(fa[j], fa[j], fmaf(fb[j], fb[j], ss));
+#pragma unroll
+            for (int d = LPH / 2; d >= 1; d >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, d);
+            if (!on || h >= H) continue;
+            T* dst = is_q ? static_cast<T*>(p.q_out) + (static_cast<long long>(i) * p.Hq + h) * D
+                          : static_cast<T*>(is_v ? p.v_cache : p.k_cache) +
+                                (cache_row + (is_v ? h - p.Hq - p.Hkv : h - p.Hq)) * D;
+            if (!is_v) {
+                if (wt) {
+                    const float inv = rsqrtf(ss * (1.0f / D) + p.eps);
+                    float wa[N], wb[N];
+                    Vec<T>::unpack(*reinterpret_cast<const uint4*>(wt + e0), wa);
+                    Vec<T>::unpack(*reinterpret_cast<const uint4*>(wt + e1), wb);
+#pragma unroll
+                    for (int j = 0; j < N; ++j) fa[j] *= inv * wa[j], fb[j] *= inv * wb[j];
+                }
+                if (rotated) {
+                    if (split) {
+#pragma unroll
+                        for (int j = 0; j < N; ++j) {
+                            const float x = fa[j], y = fb[j];
+                            fa[j] = x * cs[j] - y * sn[j];
+                            fb[j] = y * cs[j] + x * sn[j];
+                        }
+                    } else {  // fa, fb: 2 N neighbouring elements
+#pragma unroll
+                        for (int j = 0; j < N / 2; ++j) {
+                            const float x = fa[2 * j], y = fa[2 * j + 1], z = fb[2 * j], w = fb[2 * j + 1];
+                            fa[2 * j] = x * cs[j] - y * sn[j];
+                            fa[2 * j + 1] = y * cs[j] + x * sn[j];
+                            fb[2 * j] = z * cs[N / 2 + j] - w * sn[N / 2 + j];
+                            fb[2 * j + 1] = w * cs[N / 2 + j] + z * sn[N / 2 + j];
+                        }
+                    }
+                }
+                if (wt || rotated) {
+                    va[q] = Vec<T>::pack(fa);
+                    vb[q] = Vec<T>::pack(fb);
+                }
+            }
+            *reinterpret_cast<uint4*>(dst + e0) = va[q];
+            *reinterpret_cast<uint4*>(dst + e1) = vb[q];
+        }
+    }
+}
+
+template <typename T, int D>
+static cudaError_t append_launch(Append prm, cudaStream_t st) {
+    constexpr int active = D / 2 / Vec<T>::N;
+    constexpr int LPH = active <= 4 ? 4 : active <= 8 ? 8 : 16;
+    static_assert(active <= 16, "head dim");
+    const int H = prm.Hq + 2 * prm.Hkv, per = 32 / LPH;
+    // Few tokens: one head per lane group, so that a token's heads are read at
+    // once; many: four heads in flight per group, which amortises the token's
+    // offsets, page and angles.
+    const int fine = (H + per - 1) / per, coarse = (H + per * kUnroll - 1) / (per * kUnroll);
+    prm.warps_per_token = static_cast<long long>(prm.total) * fine <= 16ll * device_sm_count() ? fine : coarse;
+    const long long warps = static_cast<long long>(prm.total) * prm.warps_per_token;
+    const long long blocks = (warps + kAppendThreads / 32 - 1) / (kAppendThreads / 32);
+    if (blocks > 0x7FFFFFFFll) return cudaErrorInvalidValue;
+    return launch_kernel_pdl(qkv_append_kernel<T, D, LPH>, dim3(static_cast<unsigned>(blocks)), dim3(kAppendThreads), 0,
+                             st, prm);
+}
+
+// ---------------------------------------------------------------------------
+// kv_commit: for d = 1 .. accept_len[b], slot L_b + d <- slot L_b + path[b, d]
+// in every layer, K and V; new_prefix[b] = L_b + accept_len[b] + 1.
+//
+// The path rises strictly, so path[d] >= d and a step's source is never a slot
+// that an earlier step wrote unless it is its own target: walking d upwards in
+// place is safe, and so is loading a batch of steps before storing it.  A slot's
+// heads are one contiguous row; a thread moves one 16-byte column of it, with
+// the row offsets of the whole path worked out once per CTA.  grid (nseq,
+// layer-halves): a CTA takes every gridDim.y-th of the 2 * layers caches.
+// Bound: HBM bytes of the moved rows; for one sequence the chain accept_len ->
+// path -> page -> row.
+// ---------------------------------------------------------------------------
+struct Commit {
+    char* k_cache;
+    char* v_cache;
+    const int32_t* block_table;
+    const int32_t* prefix_len;
+    const int32_t* off;
+    const int32_t* accept_len;
+    const int32_t* path;
+    int32_t* new_prefix;
+    int32_t* staged;        // [nseq]: new lengths, when new_prefix is prefix_len
+    uint32_t* err;
+    uint32_t* arrivals;     // workspace header word, 0 between calls
+    long long layer_stride;
+    int row_bytes, layers, max_pages, num_pages, nseq, N, in_place;
+};
+
+constexpr int kCommitThreads = 128;
+constexpr int kCommitBatch = 8;
+
+__global__ void __launch_bounds__(kCommitThreads) kv_commit_kernel(const Commit p) {
+    __shared__ long long src[JT_MAX_TREE], dst[JT_MAX_TREE];
+    __shared__ int last;
+    pdl_wait();
+    pdl_trigger();
+    const int b = blockIdx.x, tid = threadIdx.x;
+    const int acc = p.accept_len[b], L = p.prefix_len[b], B = p.off[b + 1] - p.off[b];
+    const int32_t* path = p.path + static_cast<long long>(b) * (p.N + 1);
+    bool ok = acc >= 0 && acc <= p.N && B >= 1 && B <= JT_MAX_TREE && acc < B && L >= 0 &&
+              static_cast<long long>(L) + B <=
+                  min(static_cast<long long>(p.max_pages) * JT_PAGE_SIZE, 0x7FFFFF00ll);
+    if (ok) {
+        const int32_t* table = p.block_table + static_cast<long long>(b) * p.max_pages;
+        for (int d = tid; d <= acc; d += kCommitThreads) {
+            const int node = path[d], before = d > 0 ? path[d - 1] : -1;
+            if (node <= before || node >= B || (d == 0 && node != 0)) {
+                ok = false;
+            } else if (d > 0) {
+                const int sp = table[(L + node) / JT_PAGE_SIZE], dp = table[(L + d) / JT_PAGE_SIZE];
+                if (sp < 0 || sp >= p.num_pages || dp < 0 || dp >= p.num_pages) ok = false;
+                src[d - 1] = (static_cast<long long>(sp) * JT_PAGE_SIZE + (L + node) % JT_PAGE_SIZE) * p.row_bytes;
+                dst[d - 1] = (static_cast<long long>(dp) * JT_PAGE_SIZE + (L + d) % JT_PAGE_SIZE) * p.row_bytes;
+            }
+        }
+    }
+    ok = __syncthreads_and(ok);
+    if (blockIdx.y == 0 && tid == 0) {
+        if (!ok) raise_error(p.err, DEVERR_INVALID);
+        if (p.in_place)
+            p.staged[b] = ok ? L + acc + 1 : L;
+        else if (ok)
+            p.new_prefix[b] = L + acc + 1;
+    }
+    if (p.in_place && tid == 0) {
+        // Every CTA has read its old length by the time it arrives: the last to
+        // arrive may overwrite them, and leaves the count at 0 for the next call.
+        __threadfence();
+        const uint32_t n = gridDim.x * gridDim.y;
+        last = atomicAdd(p.arrivals, 1u) == n - 1u;
+        if (last) *p.arrivals = 0u;
+        __threadfence();
+    }
+    if (ok) {
+        for (int c = blockIdx.y; c < 2 * p.layers; c += gridDim.y) {
+            char* cache = (c & 1 ? p.v_cache : p.k_cache) + (c >> 1) * p.layer_stride;
+            for (int col = tid * 16; col < p.row_bytes; col += kCommitThreads * 16) {
+                for (int d0 = 0; d0 < acc; d0 += kCommitBatch) {
+                    uint4 v[kCommitBatch];
+#pragma unroll
+                    for (int k = 0; k < kCommitBatch; ++k)
+                        if (d0 + k < acc && src[d0 + k] != dst[d0 + k])
+                            v[k] = *reinterpret_cast<const uint4*>(cache + src[d0 + k] + col);
+#pragma unroll
+                    for (int k = 0; k < kCommitBatch; ++k)
+                        if (d0 + k < acc && src[d0 + k] != dst[d0 + k])
+                            *reinterpret_cast<uint4*>(cache + dst[d0 + k] + col) = v[k];
+                }
+            }
+        }
+    }
+    if (p.in_place) {
+        __syncthreads();
+        if (last)
+            for (int i = tid; i < p.nseq; i += kCommitThreads)
+                p.new_prefix[i] = *static_cast<volatile int32_t*>(p.staged + i);
+    }
+}
+
+}  // namespace kv
+
+cudaError_t qkv_append_launch(const AppendArgs& a, uint32_t* err, cudaStream_t st) {
+    kv::Append p;
+    p.qkv = a.qkv;
+    p.q_weight = a.q_weight;
+    p.k_weight = a.k_weight;
+    p.cos_sin = a.cos_sin;
+    p.depth = a.depth;
+    p.block_table = a.block_table;
+    p.prefix_len = a.prefix_len;
+    p.off = a.tree_off;
+    p.q_out = a.q_out;
+    p.k_cache = a.k_cache;
+    p.v_cache = a.v_cache;
+    p.err = err;
+    p.row_stride = a.row_stride;
+    p.max_pos = a.max_pos;
+    p.rot = a.rot_dim;
+    p.interleaved = a.interleaved;
+    p.max_pages = a.max_pages;
+    p.num_pages = a.num_pages;
+    p.nseq = a.nseq;
+    p.total = a.total;
+    p.Hq = a.Hq;
+    p.Hkv = a.Hkv;
+    p.warps_per_token = 1;
+    p.eps = a.eps;
+    if (a.dtype == JT_DTYPE_BF16) {
+        if (a.D == 64) return kv::append_launch<__nv_bfloat16, 64>(p, st);
+        if (a.D == 128) return kv::append_launch<__nv_bfloat16, 128>(p, st);
+        return cudaErrorInvalidValue;
+    }
+    switch (a.D) {
+        case 32: return kv::append_launch<float, 32>(p, st);
+        case 64: return kv::append_launch<float, 64>(p, st);
+        case 96: return kv::append_launch<float, 96>(p, st);
+        case 128: return kv::append_launch<float, 128>(p, st);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+size_t kv_commit_workspace_bytes(int nseq) { return kWsHeader + align_up(static_cast<size_t>(nseq) * sizeof(int32_t)); }
+
+cudaError_t kv_commit_launch(const CommitArgs& a, char* ws, cudaStream_t st) {
+    kv::Commit p;
+    p.k_cache = static_cast<char*>(a.k_cache);
+    p.v_cache = static_cast<char*>(a.v_cache);
+    p.block_table = a.block_table;
+    p.prefix_len = a.prefix_len;
+    p.off = a.tree_off;
+    p.accept_len = a.accept_len;
+    p.path = a.path;
+    p.new_prefix = a.new_prefix;
+    p.staged = reinterpret_cast<int32_t*>(ws + kWsHeader);
+    p.err = reinterpret_cast<uint32_t*>(ws);
+    p.arrivals = &reinterpret_cast<WsHeader*>(ws)->arrivals;
+    p.layer_stride = a.layer_stride;
+    p.row_bytes = a.row_bytes;
+    p.layers = a.layers;
+    p.max_pages = a.max_pages;
+    p.num_pages = a.num_pages;
+    p.nseq = a.nseq;
+    p.N = a.N;
+    p.in_place = a.new_prefix == a.prefix_len;
+    // about 16 CTAs per SM: beyond that a CTA takes several caches, so that its
+    // path's offsets serve more than one
+    const int halves = 2 * a.layers;
+    const int ctas = std::max(1, std::min(halves, 16 * device_sm_count() / std::max(1, a.nseq)));
+    return launch_kernel_pdl(kv::kv_commit_kernel, dim3(a.nseq, std::min(ctas, 65535)), dim3(kv::kCommitThreads), 0, st,
+                             p);
+}
+
+}  // namespace jt
