@@ -136,12 +136,12 @@ def jt_version() -> int:
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    # a plain int: every pointer argument's argtype is c_void_p
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream=None):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
 
 
 def _need(t, name, dtype, device=None):
@@ -149,7 +149,7 @@ def _need(t, name, dtype, device=None):
         raise TypeError(f"{name} must be a torch tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (libjt has no CPU path)")
-    if dtype is not None and t.dtype != dtype:
+    if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -161,12 +161,19 @@ def _check(rc, where):
         raise JtError(rc, where)
 
 
-def _tensors(obj):
-    if isinstance(obj, torch.Tensor):
-        yield obj
-    elif isinstance(obj, (tuple, list)):
-        for o in obj:
-            yield from _tensors(o)
+def _device_of(objs, idx, where):
+    """The device index of the CUDA tensors among objs (nested tuples and lists
+    included), or idx when there is none; refuses a second device."""
+    for o in objs:
+        if isinstance(o, torch.Tensor):
+            i = o.get_device()
+            if i >= 0 and i != idx:
+                if idx >= 0:
+                    raise ValueError(f"{where}: tensors on several devices (cuda:{idx}, cuda:{i})")
+                idx = i
+        elif isinstance(o, (tuple, list)):
+            idx = _device_of(o, idx, where)
+    return idx
 
 
 def _on_tensor_device(fn):
@@ -176,12 +183,10 @@ def _on_tensor_device(fn):
     current one is moved there; tensors on different devices are refused."""
     @functools.wraps(fn)
     def wrapper(*args, **kwargs):
-        devs = {t.device for t in _tensors(list(args) + list(kwargs.values())) if t.is_cuda}
-        if len(devs) > 1:
-            raise ValueError(f"{fn.__name__}: tensors on several devices ({sorted(map(str, devs))})")
-        if not devs:
+        idx = _device_of(kwargs.values(), _device_of(args, -1, fn.__name__), fn.__name__)
+        if idx < 0 or idx == torch.cuda.current_device():
             return fn(*args, **kwargs)
-        with torch.cuda.device(devs.pop()):
+        with torch.cuda.device(idx):
             return fn(*args, **kwargs)
     return wrapper
 

@@ -946,11 +946,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         Piece pc;
         int cnt = 0, npc = 0;               // tiles and pieces so far
         uint32_t mph = 0, own_seen = 0, own_par = 0;  // m_bar phase parities per tile parity; v_own phases
-        int xph = 0;
         auto meet8 = [&](int i) -> bool {   // meeting i of a merge (a merge meets twice: parity i)
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars->msync);
             return mbar_wait_warp(&bars->msync, static_cast<uint32_t>(i), p.err, abort);
+        };
+        // the partner warp has decided on the maxima after tile t - 1 / this one has after tile t
+        auto partner_done = [&](int t) -> bool {
+            const int o = (t - 1) & 1;
+            return mbar_wait_warp(&bars->m_bar[w4][o], ((mph >> o) & 1u) ^ 1u, p.err, abort);
+        };
+        auto tell_partner = [&](int t) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->m_bar[w4][t & 1]);
+            mph ^= 1u << (t & 1);
         };
         bool ok = true;
         while (ok && w.next(p, pc)) {
@@ -965,8 +974,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             float m_run = -INFINITY, l_run = 0.0f;
             for (int j = 0; j < pc.nt; ++j, ++cnt) {
                 const int b = cnt % 3;
-                const bool mine = (cnt & 1) == wg;
-                if (!mine && warp_on) {
+                if ((cnt & 1) != wg) {
                     mph ^= 1u << (cnt & 1);  // the other warpgroup's tile: one more phase of its m_bar
                     continue;
                 }
@@ -974,7 +982,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     ok = false;
                     break;
                 }
-                if (!mine) continue;
                 tc_fence_after();
                 if (warp_on) {
                     const uint32_t tS = tmem + 128 * b + lane_off;
@@ -983,16 +990,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     load_srow(tS, sr);
                     if (slot0 + kTileN > first_masked) mask_srow(sr, L + token + 1 - slot0);
                     const float mx_s = max_srow(sr) * sl2;
-                    // the row's maximum after the tile before, from the partner warp
-                    float m_prev = -INFINITY;
-                    if (j > 0) {
-                        const int o = (cnt - 1) & 1;
-                        if (!mbar_wait_warp(&bars->m_bar[w4][o], ((mph >> o) & 1u) ^ 1u, p.err, abort)) {
-                            ok = false;
-                            break;
-                        }
-                        m_prev = mbuf[o * 128 + r];
+                    if (j > 0 && !partner_done(cnt)) {
+                        ok = false;
+                        break;
                     }
+                    // the row's maximum after the tile before, from the partner warp
+                    const float m_prev = j > 0 ? mbuf[((cnt - 1) & 1) * 128 + r] : -INFINITY;
                     float m_new = m_prev, factor = 1.0f;
                     bool resc = false;
                     if (mx_s > m_prev + kRescaleLog2 || m_prev == -INFINITY) {
@@ -1001,9 +1004,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         if (resc) factor = ex2_approx(m_prev - m_new);
                     }
                     mbuf[(cnt & 1) * 128 + r] = m_new;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bars->m_bar[w4][cnt & 1]);
-                    mph ^= 1u << (cnt & 1);
+                    tell_partner(cnt);
                     if (m_new != m_run) {  // this warp's part of the sum follows
                         l_run = m_run == -INFINITY ? 0.0f : l_run * ex2_approx(m_run - m_new);
                         m_run = m_new;
@@ -1028,6 +1029,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         }
                     }
                     tmem_wait_st();
+                } else {
+                    // Warps without rows keep step all the same: a warp waits
+                    // only for its own tiles' S, and what it has seen of its
+                    // partner covers the phases in between.
+                    if (j > 0 && !partner_done(cnt)) {
+                        ok = false;
+                        break;
+                    }
+                    tell_partner(cnt);
                 }
                 if (pc.t0 + j == pc.T - 1 && w4 == 0) {
                     // the unit's final tile: zero the rows of its last page past the last needed slot
@@ -1055,24 +1065,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             if (w.remaining <= 0) pdl_trigger();
             // ------------------------------------------- end of the piece
-            float m_tot = -INFINITY, l_tot = 0.0f;
-            if (warp_on) {
-                // both warps of the rows: whole maxima and sums
-                float2* xp = xch + (npc & 1) * 64;
-                xp[wg * 32 + lane] = make_float2(m_run, l_run);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars->x_bar[w4]);
-                if (!mbar_wait_warp(&bars->x_bar[w4], xph & 1, p.err, abort)) {
-                    ok = false;
-                    break;
-                }
-                ++xph;
-                const float2 a = xp[lane], c = xp[32 + lane];  // in this order for both warps
-                m_tot = fmaxf(a.x, c.x);
-                const float fa = a.x == -INFINITY ? 0.0f : ex2_approx(a.x - m_tot);
-                const float fc = c.x == -INFINITY ? 0.0f : ex2_approx(c.x - m_tot);
-                l_tot = a.y * fa + c.y * fc;
+            // both warps of the rows: whole maxima and sums
+            float2* xp = xch + (npc & 1) * 64;
+            xp[wg * 32 + lane] = make_float2(m_run, l_run);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->x_bar[w4]);
+            if (!mbar_wait_warp(&bars->x_bar[w4], npc & 1, p.err, abort)) {
+                ok = false;
+                break;
             }
+            const float2 xa = xp[lane], xb = xp[32 + lane];  // in this order for both warps
+            const float m_tot = fmaxf(xa.x, xb.x);
+            const float l_tot = (xa.x == -INFINITY ? 0.0f : xa.y * ex2_approx(xa.x - m_tot)) +
+                                (xb.x == -INFINITY ? 0.0f : xb.y * ex2_approx(xb.x - m_tot));
             ++npc;
             if (!mbar_wait_warp(&bars->o_done[(cnt - 1) % 3], ((cnt - 1) / 3) & 1, p.err, abort)) {
                 ok = false;
