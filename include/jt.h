@@ -524,6 +524,17 @@ jt_status jt_kv_commit(void* k_cache, void* v_cache, int dtype, int layers, int6
                        jt_stream_t stream);
 
 /*
+ * jt_call -- jt_qkv_append, jt_chunk_attn_paged or jt_kv_commit with its
+ * arguments in one block of memory, for bindings that pay per argument
+ * (single-token calls are bound by the host).
+ *   op:    JT_OP_QKV_APPEND, JT_OP_CHUNK_ATTN or JT_OP_KV_COMMIT.
+ *   args:  host; a struct whose members have the types and order of the entry
+ *          point's parameters, laid out as the C compiler does.
+ *   bytes: its size, checked (JT_ERR_INVALID).
+ */
+jt_status jt_call(int op, const void* args, size_t bytes);
+
+/*
  * jt_check -- synchronise `stream`, read the device-side error flag of a
  * workspace used by an earlier call, clear it, and return the matching
  * status (JT_OK, JT_ERR_INVALID, JT_ERR_TIMEOUT or JT_ERR_CUDA).

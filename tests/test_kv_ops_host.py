@@ -6,16 +6,33 @@ import ctypes
 import pytest
 
 import tree_speculative_decoding_jt_gb300 as jt
+from tree_speculative_decoding_jt_gb300 import binding
 
 A, B, C = (ctypes.c_void_p(4096 * i) for i in (1, 2, 3))
 ODD = ctypes.c_void_p(4096 + 8)
 INVALID, UNSUPPORTED, WORKSPACE = jt.JT_ERR_INVALID, jt.JT_ERR_UNSUPPORTED, jt.JT_ERR_WORKSPACE
 
 
+OPS = dict(jt_qkv_append=jt.JT_OP_QKV_APPEND, jt_chunk_attn_paged=jt.JT_OP_CHUNK_ATTN, jt_kv_commit=jt.JT_OP_KV_COMMIT)
+
+
 def call(name, defaults, **change):
+    """The entry point's status, and the same through jt_call's packed arguments."""
     assert set(change) <= set(defaults), change
-    args = {**defaults, **change}
-    return getattr(jt.load(), name)(*args.values())
+    args = list({**defaults, **change}.values())
+    rc = getattr(jt.load(), name)(*args)
+    s = binding._PACK[OPS[name]]
+    packed = s.pack(*((a.value if isinstance(a, ctypes.c_void_p) else a or 0) for a in args))
+    assert jt.load().jt_call(OPS[name], packed, s.size) == rc
+    return rc
+
+
+def test_packed_calls_of_another_size_or_operator_are_refused():
+    s = binding._PACK[jt.JT_OP_KV_COMMIT]
+    lib = jt.load()
+    assert lib.jt_call(jt.JT_OP_KV_COMMIT, bytes(s.size), s.size - 8) == jt.JT_ERR_INVALID
+    assert lib.jt_call(jt.JT_OP_KV_COMMIT, None, s.size) == jt.JT_ERR_INVALID
+    assert lib.jt_call(jt.JT_OP_TREE_ATTN, bytes(s.size), s.size) == jt.JT_ERR_INVALID
 
 
 APPEND = dict(qkv=A, dtype=1, row_stride=6144, q_weight=None, k_weight=None, eps=1e-6, cos_sin=A, max_pos=100,

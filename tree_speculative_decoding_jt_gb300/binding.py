@@ -13,6 +13,7 @@ import ctypes
 import functools
 import math
 import os
+import struct
 import threading
 
 import torch
@@ -31,7 +32,7 @@ EXPORTS = ("jt_workspace_size", "jt_tree_build", "jt_tree_topw", "jt_tree_expand
            "jt_tree_attn_paged", "jt_verify_accept", "jt_check", "jt_status_str", "jt_version",
            "jt_tree_build_noalloc", "jt_verify_accept_stochastic", "jt_tree_build_mixed",
            "jt_tree_expand_capped", "jt_tree_policy", "jt_tree_build_adaptive", "jt_selftest_wait_timeout",
-           "jt_qkv_append", "jt_chunk_attn_paged", "jt_kv_commit")
+           "jt_qkv_append", "jt_chunk_attn_paged", "jt_kv_commit", "jt_call")
 
 _lock = threading.Lock()
 _lib = None
@@ -112,6 +113,7 @@ def load(build_if_missing: bool = True):
                                             f32, P, P, P, sz, P]
         lib.jt_kv_commit.argtypes = [P, P, i32, i32, i64, P, i32, i32, P, P, P, P, i32, i32, i32, i32, i32, P, P,
                                      sz, P]
+        lib.jt_call.argtypes = [i32, ctypes.c_char_p, sz]
         lib.jt_check.argtypes = [P, P]
         lib.jt_selftest_wait_timeout.argtypes = [P, sz, P]
         lib.jt_status_str.argtypes = [i32]
@@ -121,7 +123,7 @@ def load(build_if_missing: bool = True):
                      "jt_verify_accept", "jt_check", "jt_version", "jt_tree_build_noalloc",
                      "jt_verify_accept_stochastic", "jt_tree_build_mixed", "jt_tree_expand_capped",
                      "jt_tree_policy", "jt_tree_build_adaptive", "jt_selftest_wait_timeout", "jt_qkv_append",
-                     "jt_chunk_attn_paged", "jt_kv_commit"):
+                     "jt_chunk_attn_paged", "jt_kv_commit", "jt_call"):
             getattr(lib, name).restype = i32
         _lib = lib
         return lib
@@ -543,38 +545,71 @@ def jt_verify_accept(target_logits, parent, token, tree_off, N, rule=JT_RULE_GRE
     return acc, path, bonus
 
 
-def _dtype_of(t, name):
-    if t.dtype == torch.bfloat16:
-        return JT_DTYPE_BF16
-    if t.dtype == torch.float32:
-        return JT_DTYPE_F32
-    raise TypeError(f"{name} must be bf16 or fp32")
+# The cache operators run once per layer and token, where the host's time per
+# call counts: one pass of checks per tensor, the arguments packed for jt_call.
+_PACK = {op: struct.Struct(fmt) for op, fmt in (
+    (JT_OP_QKV_APPEND, "@PiqPPfPiiiPPiiPPiiiiiiPPPPNP"),
+    (JT_OP_CHUNK_ATTN, "@PPPiPiiPPiiiiiiifPPPNP"),
+    (JT_OP_KV_COMMIT, "@PPiiqPiiPPPPiiiiiPPNP"))}
+_FLOATS = {torch.bfloat16: JT_DTYPE_BF16, torch.float32: JT_DTYPE_F32}
 
 
-def _shape(t, name, shape):
-    if tuple(t.shape) != tuple(shape):
+def _lead(t, name):
+    """Device index and jt dtype of the tensor that sets both for a call."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    dtype = _FLOATS.get(t.dtype)
+    if dtype is None:
+        raise TypeError(f"{name} must be bf16 or fp32")
+    idx = t.get_device()
+    if idx < 0:
+        raise ValueError(f"{name} must be a CUDA tensor (libjt has no CPU path)")
+    return idx, dtype
+
+
+def _like(t, name, dtype, idx, shape):
+    """Check a contiguous tensor of the call's device, a type and a shape."""
+    if (not isinstance(t, torch.Tensor) or t.get_device() != idx or t.dtype is not dtype or t.shape != shape
+            or not t.is_contiguous()):
+        _need(t, name, dtype)
+        if t.get_device() != idx:
+            raise ValueError(f"{name}: tensors on several devices (cuda:{idx}, cuda:{t.get_device()})")
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    return t
 
 
-def _caches(k_cache, v_cache, dtype, dims=(4,)):
-    _need(k_cache, "k_cache", dtype)
-    _need(v_cache, "v_cache", dtype)
-    if k_cache.dim() not in dims:
-        raise ValueError(f"k_cache must have {' or '.join(map(str, dims))} dimensions, got {k_cache.dim()}")
-    _shape(v_cache, "v_cache", k_cache.shape)
-
-
-def _batch(block_table, prefix_len, off, off_name):
-    _need(block_table, "block_table", torch.int32)
-    _need(prefix_len, "prefix_len", torch.int32)
-    _need(off, off_name, torch.int32)
-    if block_table.dim() != 2:
-        raise ValueError("block_table must have 2 dimensions")
-    nseq, max_pages = block_table.shape
-    _shape(prefix_len, "prefix_len", (nseq,))
-    _shape(off, off_name, (nseq + 1,))
+def _tables(block_table, prefix_len, off, off_name, idx):
+    """(nseq, max_pages) of a batch's checked tables."""
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError("block_table must be a tensor of 2 dimensions")
+    shape = block_table.shape
+    _like(block_table, "block_table", torch.int32, idx, shape)
+    nseq, max_pages = shape
+    _like(prefix_len, "prefix_len", torch.int32, idx, (nseq,))
+    _like(off, off_name, torch.int32, idx, (nseq + 1,))
     return nseq, max_pages
+
+
+def _workspace_of(ws, idx):
+    if not isinstance(ws, torch.Tensor) or ws.get_device() != idx or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous tensor on cuda:{idx}")
+    return ws.numel() * ws.element_size()
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # no Stream object made
+
+
+def _packed(op, idx, stream, *args):
+    """jt_call on the tensors' device and its current stream (or the given one)."""
+    lib = load()
+    s = _PACK[op]
+    if idx != torch.cuda.current_device():
+        with torch.cuda.device(idx):
+            return lib.jt_call(op, s.pack(*args, _stream(stream)), s.size)
+    if stream is None and _raw_stream is not None:
+        raw = _raw_stream(idx)
+    else:
+        raw = _stream(stream)
+    return lib.jt_call(op, s.pack(*args, raw), s.size)
 
 
 def rope_table(max_pos, rot_dim, theta=1e6, device=None):
@@ -586,7 +621,6 @@ def rope_table(max_pos, rot_dim, theta=1e6, device=None):
     return torch.cat([a.cos(), a.sin()], 1).float().to(device or "cuda")
 
 
-@_on_tensor_device
 def jt_qkv_append(qkv, Hq, k_cache, v_cache, block_table, prefix_len, tree_off, q_weight=None, k_weight=None,
                   eps=1e-6, cos_sin=None, interleaved=False, depth=None, q_out=None, ws=None, stream=None):
     """Per-head norm of q and k, position rotation, and the write of k and v
@@ -597,46 +631,56 @@ def jt_qkv_append(qkv, Hq, k_cache, v_cache, block_table, prefix_len, tree_off, 
     None (see rope_table); depth int32 [total] (tree nodes: position L_b +
     depth) or None (position L_b + i).  Returns q_out [total, Hq, D] (None for
     Hq = 0); the caches are updated in place."""
-    lib = load()
-    dtype = _dtype_of(qkv, "qkv")
-    if not qkv.is_cuda:
-        raise ValueError("qkv must be a CUDA tensor (libjt has no CPU path)")
-    _caches(k_cache, v_cache, qkv.dtype)
-    nseq, max_pages = _batch(block_table, prefix_len, tree_off, "tree_off")
-    num_pages, page, Hkv, D = k_cache.shape
-    if qkv.dim() != 2 or qkv.shape[1] != (Hq + 2 * Hkv) * D:
-        raise ValueError(f"qkv must be [total, (Hq + 2 Hkv) * D = {(Hq + 2 * Hkv) * D}], got {tuple(qkv.shape)}")
-    if qkv.stride(1) != 1:
-        raise ValueError("qkv's rows must be contiguous")
-    total = qkv.shape[0]
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            _shape(_need(w, name, qkv.dtype), name, (D,))
+    idx, dtype = _lead(qkv, "qkv")
+    kind, kv_shape = qkv.dtype, k_cache.shape
+    if len(kv_shape) != 4:
+        raise ValueError("k_cache must be [pages, 16, Hkv, D]")
+    _like(k_cache, "k_cache", kind, idx, kv_shape)
+    _like(v_cache, "v_cache", kind, idx, kv_shape)
+    nseq, max_pages = _tables(block_table, prefix_len, tree_off, "tree_off", idx)
+    num_pages, page, Hkv, D = kv_shape
+    width = (Hq + 2 * Hkv) * D
+    if qkv.dim() != 2 or qkv.shape[1] != width:
+        raise ValueError(f"qkv must be [total, (Hq + 2 Hkv) * D = {width}], got {tuple(qkv.shape)}")
+    total, row = qkv.shape[0], width
+    if not qkv.is_contiguous():
+        if qkv.stride(1) != 1:
+            raise ValueError("qkv's rows must be contiguous")
+        row = qkv.stride(0)
+    qw = kw = table = steps = q_ptr = 0
+    if q_weight is not None:
+        _like(q_weight, "q_weight", kind, idx, (D,))
+        qw = q_weight.data_ptr()
+    if k_weight is not None:
+        _like(k_weight, "k_weight", kind, idx, (D,))
+        kw = k_weight.data_ptr()
     max_pos = rot = 0
     if cos_sin is not None:
-        _need(cos_sin, "cos_sin", torch.float32)
-        if cos_sin.dim() != 2:
+        if not isinstance(cos_sin, torch.Tensor) or cos_sin.dim() != 2:
             raise ValueError("cos_sin must be [max_pos, rot_dim]")
         max_pos, rot = cos_sin.shape
+        _like(cos_sin, "cos_sin", torch.float32, idx, (max_pos, rot))
+        table = cos_sin.data_ptr()
     if depth is not None:
-        _shape(_need(depth, "depth", torch.int32), "depth", (total,))
-    if q_out is None and Hq > 0:
-        q_out = torch.empty((total, Hq, D), dtype=qkv.dtype, device=qkv.device)
-    elif q_out is not None:
-        _shape(_need(q_out, "q_out", qkv.dtype), "q_out", (total, Hq, D))
+        _like(depth, "depth", torch.int32, idx, (total,))
+        steps = depth.data_ptr()
+    if Hq > 0:
+        if q_out is None:
+            q_out = torch.empty((total, Hq, D), dtype=kind, device=qkv.device)
+        else:
+            _like(q_out, "q_out", kind, idx, (total, Hq, D))
+        q_ptr = q_out.data_ptr()
     if ws is None:
-        ws = workspace(jt_workspace_size(JT_OP_QKV_APPEND), qkv.device)
-    # a single row's stride is whatever the view says: any value that fits does
-    rc = lib.jt_qkv_append(_ptr(qkv), dtype, qkv.stride(0) if total > 1 else qkv.shape[1], _ptr(q_weight),
-                           _ptr(k_weight), float(eps), _ptr(cos_sin), max_pos, rot, 1 if interleaved else 0,
-                           _ptr(depth), _ptr(block_table), max_pages, num_pages, _ptr(prefix_len), _ptr(tree_off),
-                           nseq, total, Hq, Hkv, D, page, _ptr(q_out), _ptr(k_cache), _ptr(v_cache), _ptr(ws),
-                           ws.numel(), _stream(stream))
-    _check(rc, "jt_qkv_append")
+        ws = workspace(256, qkv.device)
+    rc = _packed(JT_OP_QKV_APPEND, idx, stream, qkv.data_ptr(), dtype, row, qw, kw, eps, table, max_pos, rot,
+                 1 if interleaved else 0, steps, block_table.data_ptr(), max_pages, num_pages, prefix_len.data_ptr(),
+                 tree_off.data_ptr(), nseq, total, Hq, Hkv, D, page, q_ptr, k_cache.data_ptr(), v_cache.data_ptr(),
+                 ws.data_ptr(), _workspace_of(ws, idx))
+    if rc != JT_OK:
+        raise JtError(rc, "jt_qkv_append")
     return q_out
 
 
-@_on_tensor_device
 def jt_chunk_attn_paged(q, k_cache, v_cache, block_table, prefix_len, chunk_off, scale=None, max_chunk=None,
                         out=None, lse=None, ws=None, stream=None, with_lse=True):
     """Causal attention of new tokens (chunks of any length, ragged) over a
@@ -647,15 +691,16 @@ def jt_chunk_attn_paged(q, k_cache, v_cache, block_table, prefix_len, chunk_off,
     before); chunk_off [nseq+1] int32; max_chunk: the longest chunk (an upper
     bound; None reads it from chunk_off, which waits for the device).  Returns
     (out, lse)."""
-    lib = load()
-    dtype = _dtype_of(q, "q")
-    _need(q, "q", None)
-    _caches(k_cache, v_cache, q.dtype)
-    nseq, max_pages = _batch(block_table, prefix_len, chunk_off, "chunk_off")
-    if q.dim() != 3:
-        raise ValueError("q must be [total, Hq, D]")
-    total, Hq, D = q.shape
-    num_pages, page, Hkv, D2 = k_cache.shape
+    idx, dtype = _lead(q, "q")
+    kind, q_shape, kv_shape = q.dtype, q.shape, k_cache.shape
+    if len(q_shape) != 3 or len(kv_shape) != 4:
+        raise ValueError("q must be [total, Hq, D] and k_cache [pages, 16, Hkv, D]")
+    _like(q, "q", kind, idx, q_shape)
+    _like(k_cache, "k_cache", kind, idx, kv_shape)
+    _like(v_cache, "v_cache", kind, idx, kv_shape)
+    nseq, max_pages = _tables(block_table, prefix_len, chunk_off, "chunk_off", idx)
+    total, Hq, D = q_shape
+    num_pages, page, Hkv, D2 = kv_shape
     if D2 != D:
         raise ValueError("q and k_cache head dims differ")
     if max_chunk is None:
@@ -665,22 +710,24 @@ def jt_chunk_attn_paged(q, k_cache, v_cache, block_table, prefix_len, chunk_off,
     if out is None:
         out = torch.empty_like(q)
     else:
-        _shape(_need(out, "out", q.dtype), "out", q.shape)
-    if lse is None and with_lse:
+        _like(out, "out", kind, idx, q_shape)
+    if lse is not None:
+        _like(lse, "lse", torch.float32, idx, (total, Hq))
+    elif with_lse:
         lse = torch.empty((total, Hq), dtype=torch.float32, device=q.device)
-    elif lse is not None:
-        _shape(_need(lse, "lse", torch.float32), "lse", (total, Hq))
     if ws is None:
-        ws = workspace(jt_workspace_size(JT_OP_CHUNK_ATTN, nseq, 0, 0, 0, total, Hq, Hkv, D, max_pages, max_chunk),
-                       q.device)
-    rc = lib.jt_chunk_attn_paged(_ptr(q), _ptr(k_cache), _ptr(v_cache), dtype, _ptr(block_table), max_pages,
-                                 num_pages, _ptr(prefix_len), _ptr(chunk_off), nseq, total, max_chunk, Hq, Hkv, D,
-                                 page, float(scale), _ptr(out), _ptr(lse), _ptr(ws), ws.numel(), _stream(stream))
-    _check(rc, "jt_chunk_attn_paged")
+        with torch.cuda.device(idx):  # sized for the tensors' device
+            ws = workspace(jt_workspace_size(JT_OP_CHUNK_ATTN, nseq, 0, 0, 0, total, Hq, Hkv, D, max_pages, max_chunk),
+                           q.device)
+    rc = _packed(JT_OP_CHUNK_ATTN, idx, stream, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), dtype,
+                 block_table.data_ptr(), max_pages, num_pages, prefix_len.data_ptr(), chunk_off.data_ptr(), nseq,
+                 total, max_chunk, Hq, Hkv, D, page, scale, out.data_ptr(), 0 if lse is None else lse.data_ptr(),
+                 ws.data_ptr(), _workspace_of(ws, idx))
+    if rc != JT_OK:
+        raise JtError(rc, "jt_chunk_attn_paged")
     return out, lse
 
 
-@_on_tensor_device
 def jt_kv_commit(k_cache, v_cache, block_table, prefix_len, tree_off, accept_len, path, new_prefix=None, ws=None,
                  stream=None):
     """Move the accepted path's keys and values behind the prefix and advance
@@ -690,26 +737,32 @@ def jt_kv_commit(k_cache, v_cache, block_table, prefix_len, tree_off, accept_len
     updated in place); accept_len [nseq], path [nseq, N+1] int32 as
     jt_verify_accept returns them; new_prefix: int32 [nseq] output, prefix_len
     itself to update it in place, None for a new tensor.  Returns new_prefix."""
-    lib = load()
-    dtype = _dtype_of(k_cache, "k_cache")
-    _caches(k_cache, v_cache, k_cache.dtype, (4, 5))
-    nseq, max_pages = _batch(block_table, prefix_len, tree_off, "tree_off")
-    _shape(_need(accept_len, "accept_len", torch.int32), "accept_len", (nseq,))
-    _need(path, "path", torch.int32)
-    if path.dim() != 2 or path.shape[0] != nseq:
-        raise ValueError(f"path must be [{nseq}, N+1]")
-    num_pages, page, Hkv, D = k_cache.shape[-4:]
-    layers = k_cache.shape[0] if k_cache.dim() == 5 else 1
+    idx, dtype = _lead(k_cache, "k_cache")
+    kv_shape = k_cache.shape
+    if len(kv_shape) not in (4, 5):
+        raise ValueError("k_cache must be [pages, 16, Hkv, D] or [layers, pages, 16, Hkv, D]")
+    _like(k_cache, "k_cache", k_cache.dtype, idx, kv_shape)
+    _like(v_cache, "v_cache", k_cache.dtype, idx, kv_shape)
+    nseq, max_pages = _tables(block_table, prefix_len, tree_off, "tree_off", idx)
+    _like(accept_len, "accept_len", torch.int32, idx, (nseq,))
+    if not isinstance(path, torch.Tensor) or path.dim() != 2:
+        raise ValueError("path must be [nseq, N+1]")
+    width = path.shape[1]
+    _like(path, "path", torch.int32, idx, (nseq, width))
+    num_pages, page, Hkv, D = kv_shape[-4:]
+    layers = kv_shape[0] if len(kv_shape) == 5 else 1
     if new_prefix is None:
         new_prefix = torch.empty_like(prefix_len)
-    else:
-        _shape(_need(new_prefix, "new_prefix", torch.int32), "new_prefix", (nseq,))
+    elif new_prefix is not prefix_len:
+        _like(new_prefix, "new_prefix", torch.int32, idx, (nseq,))
     if ws is None:
         ws = workspace(jt_workspace_size(JT_OP_KV_COMMIT, nseq), k_cache.device)
-    rc = lib.jt_kv_commit(_ptr(k_cache), _ptr(v_cache), dtype, layers, num_pages * page * Hkv * D, _ptr(block_table),
-                          max_pages, num_pages, _ptr(prefix_len), _ptr(tree_off), _ptr(accept_len), _ptr(path), nseq,
-                          path.shape[1] - 1, Hkv, D, page, _ptr(new_prefix), _ptr(ws), ws.numel(), _stream(stream))
-    _check(rc, "jt_kv_commit")
+    rc = _packed(JT_OP_KV_COMMIT, idx, stream, k_cache.data_ptr(), v_cache.data_ptr(), dtype, layers,
+                 num_pages * page * Hkv * D, block_table.data_ptr(), max_pages, num_pages, prefix_len.data_ptr(),
+                 tree_off.data_ptr(), accept_len.data_ptr(), path.data_ptr(), nseq, width - 1, Hkv, D, page,
+                 new_prefix.data_ptr(), ws.data_ptr(), _workspace_of(ws, idx))
+    if rc != JT_OK:
+        raise JtError(rc, "jt_kv_commit")
     return new_prefix
 
 

@@ -449,6 +449,86 @@ jt_status jt_kv_commit(void* k_cache, void* v_cache, int dtype, int layers, int6
     return from_cuda(kv_commit_launch(a, static_cast<char*>(ws), stream));
 }
 
+jt_status jt_call(int op, const void* args, size_t bytes) {
+    struct Append {
+        const void* qkv;
+        int dtype;
+        int64_t row_stride;
+        const void* q_weight;
+        const void* k_weight;
+        float eps;
+        const float* cos_sin;
+        int max_pos, rot_dim, interleaved;
+        const int32_t* depth;
+        const int32_t* block_table;
+        int max_pages, num_pages;
+        const int32_t* prefix_len;
+        const int32_t* tree_off;
+        int nseq, total_nodes, Hq, Hkv, D, page_size;
+        void* q_out;
+        void* k_cache;
+        void* v_cache;
+        void* ws;
+        size_t ws_bytes;
+        jt_stream_t stream;
+    };
+    struct Chunk {
+        const void* q;
+        const void* k_cache;
+        const void* v_cache;
+        int dtype;
+        const int32_t* block_table;
+        int max_pages, num_pages;
+        const int32_t* prefix_len;
+        const int32_t* chunk_off;
+        int nseq, total_tokens, max_chunk, Hq, Hkv, D, page_size;
+        float scale;
+        void* out;
+        float* lse;
+        void* ws;
+        size_t ws_bytes;
+        jt_stream_t stream;
+    };
+    struct Commit {
+        void* k_cache;
+        void* v_cache;
+        int dtype, layers;
+        int64_t layer_stride;
+        const int32_t* block_table;
+        int max_pages, num_pages;
+        const int32_t* prefix_len;
+        const int32_t* tree_off;
+        const int32_t* accept_len;
+        const int32_t* path;
+        int nseq, N, Hkv, D, page_size;
+        int32_t* new_prefix;
+        void* ws;
+        size_t ws_bytes;
+        jt_stream_t stream;
+    };
+    if (!args) return JT_ERR_INVALID;
+    if (op == JT_OP_QKV_APPEND && bytes == sizeof(Append)) {
+        const Append& a = *static_cast<const Append*>(args);
+        return jt_qkv_append(a.qkv, a.dtype, a.row_stride, a.q_weight, a.k_weight, a.eps, a.cos_sin, a.max_pos,
+                             a.rot_dim, a.interleaved, a.depth, a.block_table, a.max_pages, a.num_pages, a.prefix_len,
+                             a.tree_off, a.nseq, a.total_nodes, a.Hq, a.Hkv, a.D, a.page_size, a.q_out, a.k_cache,
+                             a.v_cache, a.ws, a.ws_bytes, a.stream);
+    }
+    if (op == JT_OP_CHUNK_ATTN && bytes == sizeof(Chunk)) {
+        const Chunk& a = *static_cast<const Chunk*>(args);
+        return jt_chunk_attn_paged(a.q, a.k_cache, a.v_cache, a.dtype, a.block_table, a.max_pages, a.num_pages,
+                                   a.prefix_len, a.chunk_off, a.nseq, a.total_tokens, a.max_chunk, a.Hq, a.Hkv, a.D,
+                                   a.page_size, a.scale, a.out, a.lse, a.ws, a.ws_bytes, a.stream);
+    }
+    if (op == JT_OP_KV_COMMIT && bytes == sizeof(Commit)) {
+        const Commit& a = *static_cast<const Commit*>(args);
+        return jt_kv_commit(a.k_cache, a.v_cache, a.dtype, a.layers, a.layer_stride, a.block_table, a.max_pages,
+                            a.num_pages, a.prefix_len, a.tree_off, a.accept_len, a.path, a.nseq, a.N, a.Hkv, a.D,
+                            a.page_size, a.new_prefix, a.ws, a.ws_bytes, a.stream);
+    }
+    return JT_ERR_INVALID;
+}
+
 jt_status jt_check(void* ws, jt_stream_t stream) {
     JT_RANGE("jt_check");
     if (!ws) return JT_ERR_WORKSPACE;
