@@ -26,20 +26,21 @@
 //
 // Warps per CTA (384 threads; warp 11 idles):
 //   0-3 / 4-7  softmax of the tiles with even / odd number, one query row per
-//              thread.  Warps w and w + 4 hold the same 32 rows: the running
-//              maximum of a row goes from one to the other through shared
-//              memory, tile by tile (m_bar), and each keeps its own part of
-//              the sum.  So each warp has two tiles' time for one tile's
-//              softmax, which a single warp per row had not: the tensor pipe
-//              sets the pace.  O is rescaled only when a row's maximum grows by
-//              more than 2^32: P then stays below 2^32 and O and l far inside
-//              fp32.  Warps whose rows are all past the chunk's end (single
-//              tokens fill 1 to 16 of 256 rows) compute nothing.
+//              thread.  Warps w and w + 4 hold the same 32 rows, and each warp
+//              has two tiles' time for one tile's softmax.  P of all tiles of a
+//              row is relative to one maximum m: each warp keeps the largest it
+//              knows, tells the other after every tile (m_bar) and its own part
+//              of the sum.  m is the first tile's maximum, raised only when a
+//              later score exceeds it by 2^32: P, O and l then stay far inside
+//              fp32, with no loss of relative precision, and the partner's m is
+//              not on the way of a tile's exponentials.  Warps whose rows are
+//              all past the chunk's end (single tokens fill 1 to 16 of 256 rows)
+//              compute nothing.
 //   8 / 10     TMA producers of Q and K / of V, one box per 16-token page;
 //   9          TMEM allocation; in the pair's leader, the MMA issuer.
 // TMEM (512 columns): S0, S1, S2 (P of a tile overwrites the first half of its
-// S) and O.  The MMA warp issues QK up to three tiles ahead, across units; Q
-// is double buffered.
+// S) and O.  The products S run up to three tiles ahead of O's, across units;
+// Q is double buffered.
 #include <algorithm>
 
 #include "jt_common.cuh"
@@ -49,10 +50,6 @@ namespace jt {
 namespace chunk {
 
 constexpr int kThreads = 384;
-// Registers: 168 a thread at launch (three warps per SM quarter); the softmax
-// warps, which hold a whole score row, take what the others give up: 256 * 208
-// + 128 * 88 = 384 * 168.
-constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
 constexpr int kTileN = 128;  // keys per KV tile
 constexpr int kTileM = 128;  // query rows per query tile
 constexpr float kRescaleLog2 = 32.0f;
@@ -93,7 +90,8 @@ struct Smem {
     static constexpr int kBar = kStage + 8 * 2048;
     static constexpr int kM = kBar + 512;                   // running maxima [tile parity][row]
     static constexpr int kX = kM + 1024;                    // (max, sum) [row / 32][piece parity][warpgroup][lane]
-    static constexpr int kBytes = kX + 4096;
+    static constexpr int kW = kX + 4096;                    // the softmax warps' walks
+    static constexpr int kBytes = kW + 1024;
     static constexpr int kAlloc = kBytes + 1024;            // room to align the base to 1024
 };
 
@@ -242,6 +240,12 @@ struct Walker {
     }
 };
 
+struct WarpWalk {
+    Walker w;
+    Piece pc;
+};
+static_assert(8 * sizeof(WarpWalk) <= 1024, "walk block");
+
 __device__ __forceinline__ long long warp_sum(long long v) {
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
@@ -353,27 +357,6 @@ __device__ __forceinline__ uint32_t draw_call_id(unsigned long long* tickets, bo
 // ---------------------------------------------------------------------------
 // softmax helpers: one query row (128 scores) per thread
 // ---------------------------------------------------------------------------
-struct SRow {
-    uint32_t c[4][32];
-};
-
-__device__ __forceinline__ void load_srow(uint32_t tS, SRow& s) {
-    tmem_ld32(tS, s.c[0]);
-    tmem_ld32(tS + 32, s.c[1]);
-    tmem_ld32(tS + 64, s.c[2]);
-    tmem_ld32(tS + 96, s.c[3]);
-    tmem_wait_ld();
-}
-
-// Columns at or past `visible` -> -inf.
-__device__ __forceinline__ void mask_srow(SRow& s, int visible) {
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-#pragma unroll
-        for (int c = 0; c < 32; ++c)
-            if (32 * q + c >= visible) s.c[q][c] = __float_as_uint(-INFINITY);
-}
-
 __device__ __forceinline__ float ex2_approx(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -404,45 +387,77 @@ __device__ __forceinline__ void fadd2(float& d0, float& d1, float a0, float a1, 
         : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
 }
 
-// Row maximum over eight independent chains.
-__device__ __forceinline__ float max_srow(const SRow& s) {
-    float m[8];
+// The loops over the four 32-column chunks of a score row stay loops: unrolled
+// over the whole row, the softmax's code pushed the MMA warp's out of the
+// instruction caches, and the MMA warp's loop then took longer than its MMAs
+// (2000 cycles a tile where the MMAs need 1080).
+
+// Columns at or past `visible` -> -inf.
+__device__ __forceinline__ void mask_chunk(uint32_t (&c)[32], int visible) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        m[i] = fmaxf(__uint_as_float(s.c[i >> 1][(i & 1) * 16]), __uint_as_float(s.c[i >> 1][(i & 1) * 16 + 1]));
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int c = 2; c < 16; c += 2)
-            m[i] = fmax3(m[i], __uint_as_float(s.c[i >> 1][(i & 1) * 16 + c]),
-                         __uint_as_float(s.c[i >> 1][(i & 1) * 16 + c + 1]));
-    return fmaxf(fmax3(m[0], m[1], m[2]), fmax3(fmax3(m[3], m[4], m[5]), m[6], m[7]));
+    for (int i = 0; i < 32; ++i)
+        if (i >= visible) c[i] = __float_as_uint(-INFINITY);
 }
 
-// P = exp2(s * sl2 - m), packed to bf16 pairs into the first 64 columns of
-// the S region; returns the sum of the unrounded values.
-__device__ __forceinline__ float exp_store_srow(const SRow& s, uint32_t tS, float sl2, float m) {
+// Maximum of the visible scores of this thread's row.
+__device__ __forceinline__ float row_max(uint32_t tS, bool diag, int visible) {
+    float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+    for (int q = 0; q < 4; ++q) {
+        uint32_t c[32];
+        tmem_ld32(tS + 32 * q, c);
+        tmem_wait_ld();
+        if (diag) mask_chunk(c, visible - 32 * q);
+#pragma unroll
+        for (int i = 0; i < 32; i += 2)
+            m[(i >> 1) & 3] = fmax3(m[(i >> 1) & 3], __uint_as_float(c[i]), __uint_as_float(c[i + 1]));
+    }
+    return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+
+// P = exp2(s * sl2 - m), packed to bf16 pairs into the first 64 columns of the
+// S region (chunk q writes columns 16 q .. 16 q + 15, which chunks up to q have
+// been read from); returns the sum of the unrounded values.
+__device__ __forceinline__ float row_exp(uint32_t tS, bool diag, int visible, float sl2, float m) {
     float a0 = 0.0f, a1 = 0.0f, b0 = 0.0f, b1 = 0.0f;
+#pragma unroll 1
+    for (int q = 0; q < 4; ++q) {
+        uint32_t c[32], pk[16];
+        tmem_ld32(tS + 32 * q, c);
+        tmem_wait_ld();
+        if (diag) mask_chunk(c, visible - 32 * q);
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
-        uint32_t pk[8];
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-            const int c2 = (q & 1) * 8 + c;
+        for (int i = 0; i < 16; ++i) {
             float x0, x1;
-            ffma2(x0, x1, __uint_as_float(s.c[q >> 1][2 * c2]), __uint_as_float(s.c[q >> 1][2 * c2 + 1]), sl2, sl2,
-                  -m, -m);
+            ffma2(x0, x1, __uint_as_float(c[2 * i]), __uint_as_float(c[2 * i + 1]), sl2, sl2, -m, -m);
             const float e0 = ex2_approx(x0);
             const float e1 = ex2_approx(x1);
-            if (c & 1)
+            if (i & 1)
                 fadd2(b0, b1, b0, b1, e0, e1);
             else
                 fadd2(a0, a1, a0, a1, e0, e1);
-            pk[c] = pack_bf16x2(e0, e1);
+            pk[i] = pack_bf16x2(e0, e1);
         }
-        tmem_st8(tS + 8 * q, pk);
+        tmem_st16(tS + 16 * q, pk);
     }
     return (a0 + a1) + (b0 + b1);
+}
+
+// 32 * n columns of tensor memory times f (this thread's row): fp32, or bf16
+// pairs.  Out of line: it runs when a row's maximum has grown by more than 2^32.
+template <bool kPairs>
+__device__ __noinline__ void scale_tmem(uint32_t taddr, int n, float f) {
+    for (int q = 0; q < n; ++q) {
+        uint32_t v[32];
+        tmem_ld32(taddr + q * 32, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < 32; ++c)
+            v[c] = kPairs ? pack_bf16x2(__uint_as_float(v[c] << 16) * f, __uint_as_float(v[c] & 0xFFFF0000u) * f)
+                          : __float_as_uint(__uint_as_float(v[c]) * f);
+        tmem_st32(taddr + q * 32, v);
+    }
+    tmem_wait_st();
 }
 
 // Stage this warp's 32 rows' 16 * N-byte pieces (slot[N] = this thread's row)
@@ -527,9 +542,11 @@ __device__ __noinline__ void redo_row(const Params& p, int b, int L, int g, int 
 // Operand descriptors are stepped by adding the byte offset / 16 to the
 // start-address field.  The whole MMA warp calls these; one elected lane issues.
 
-// S (+)= Q K^T over the pair: D / 16 MMAs of M = 256, N = 128, K = 16.
+// S = Q K^T over the pair: D / 16 MMAs of M = 256, N = 128, K = 16; then the
+// commits that report S, the K stage and, past a piece's last tile, its Q.
 template <int D>
-__device__ __forceinline__ void issue_qk(uint32_t tS, uint64_t dq, uint64_t dk) {
+__device__ __forceinline__ void issue_qk(uint32_t tS, uint64_t dq, uint64_t dk, uint64_t* s_full, uint64_t* k_empty,
+                                         uint64_t* q_empty) {
     using SL = Smem<D>;
     constexpr uint32_t idesc = idesc_bf16_f32(2 * kTileM, kTileN, false);
     if (elect_one()) {
@@ -539,19 +556,26 @@ __device__ __forceinline__ void issue_qk(uint32_t tS, uint64_t dq, uint64_t dk) 
             const uint32_t ko = ((kk >> 2) * SL::kKChunk + (kk & 3) * 32) >> 4;
             mma_ss_pair(tS, dq + qo, dk + ko, idesc, kk > 0 ? 1u : 0u);
         }
+        mma_commit_pair(s_full);
+        mma_commit_pair(k_empty);
+        if (q_empty) mma_commit_pair(q_empty);
     }
     __syncwarp();
 }
 
 // O (+)= P V over the pair, P (bf16 pairs) in the first 64 columns of an S
-// buffer: 8 MMAs of M = 256, N = D, K = 16.
+// buffer: 8 MMAs of M = 256, N = D, K = 16; then the commits that report O (and
+// with it the S buffer) and the V stage.
 template <int D>
-__device__ __forceinline__ void issue_pv(uint32_t tO, uint32_t tP, uint64_t dv, bool accumulate) {
+__device__ __forceinline__ void issue_pv(uint32_t tO, uint32_t tP, uint64_t dv, bool accumulate, uint64_t* o_done,
+                                         uint64_t* v_empty) {
     constexpr uint32_t idesc = idesc_bf16_f32(2 * kTileM, D, true);
     if (elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < kTileN / 16; ++kk)
             mma_ts_pair(tO, tP + kk * 8, dv + kk * ((16 * Smem<D>::kVRow) >> 4), idesc, (accumulate || kk > 0) ? 1u : 0u);
+        mma_commit_pair(o_done);
+        mma_commit_pair(v_empty);
     }
     __syncwarp();
 }
@@ -741,7 +765,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int npt = p.npt;
 
     if (quota > 0 && warp >= 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         if (warp == 8) {
             // ------------------------------------------------------- TMA: Q, K
             Walker w;
@@ -803,7 +826,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             w.init(p, bars, work);
             Piece pc;
             int jj = 0;
-            uint32_t own_seen = 0, own_par = 0;  // per stage: a unit-final copy was issued; phase parity of the last
+            int fin = 0;  // unit-final tiles so far
             bool ok = true;
             while (ok && !*abort && w.next(p, pc)) {
                 const int valid_end = unit_end(pc.s, pc.mp, npt);
@@ -841,95 +864,94 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         // leader's v_full phase of this tile completes empty
                         if (lane == 0) {
                             if (rank == 0) mbar_arrive(&bars->v_full[st]);
-                            mbar_arrive_expect_tx(&bars->v_own[st], npg * (JT_PAGE_SIZE * SL::kVRow));
+                            mbar_arrive_expect_tx(&bars->v_own[fin % VS], npg * (JT_PAGE_SIZE * SL::kVRow));
                         }
                         __syncwarp();
                         if (lane < npg)
-                            tma_load_4d(vt + lane * (JT_PAGE_SIZE * SL::kVRow), &tm_v, &bars->v_own[st], c0, pc.g, 0, pid);
-                        own_par = (own_seen >> st & 1u) ? own_par ^ (1u << st) : own_par & ~(1u << st);
-                        own_seen |= 1u << st;
+                            tma_load_4d(vt + lane * (JT_PAGE_SIZE * SL::kVRow), &tm_v, &bars->v_own[fin % VS], c0, pc.g, 0, pid);
+                        ++fin;
                     }
                 }
             }
             if (*abort) {
-                for (int s = 0; s < VS; ++s)
-                    if (own_seen >> s & 1u) mbar_wait(&bars->v_own[s], own_par >> s & 1u, p.err, nullptr);
+                for (int f = max(0, fin - VS); f < fin; ++f)
+                    mbar_wait(&bars->v_own[f % VS], (f / VS) & 1, p.err, nullptr);
                 if (rank == 0)
                     for (int j = max(0, jj - VS); j < jj; ++j)
                         mbar_wait(&bars->v_full[j % VS], (j / VS) & 1, p.err, nullptr);
             }
-        } else if (warp == 9) {
-            // ------------------------------------------------------------ MMA
-            if (rank == 0) {
-                const uint64_t dq0 = smem_desc_sw128(smem_u32(sQ), 16, 1024);
-                const uint64_t dk0 = smem_desc_sw128(smem_u32(sK), 16, 1024);
-                const uint64_t dv0 = v_desc<D>(smem_u32(sV));
-                Walker wq, wv;  // the QKs run up to three tiles ahead of the PVs, across pieces
-                wq.init(p, bars, work);
-                wv.init(p, bars, work);
-                Piece pq;
-                int issued = 0, nq = -1, left_q = 0;  // QKs issued, Q piece, its tiles left
-                bool ok = true;
-                // QK of the next tile; block: wait for its operands, else return
-                // false when they have not landed yet
-                auto qk_next = [&](bool block) -> bool {
+        } else if (rank == 0 && warp == 9) {
+            // -------------------------------------------------------- MMA
+            // One thread issues both products, in an order that the tensor
+            // pipe then keeps: QK(t + 3) right behind PV(t), which frees its S
+            // buffer.  (Two issuing warps, with QK waiting for PV's completion,
+            // took 1416 us where this takes 1315: 8192 tokens on 8192.)
+            const uint64_t dq0 = smem_desc_sw128(smem_u32(sQ), 16, 1024);
+            const uint64_t dk0 = smem_desc_sw128(smem_u32(sK), 16, 1024);
+            const uint64_t dv0 = v_desc<D>(smem_u32(sV));
+            Walker w;  // of the QKs, which run up to three tiles ahead of the PVs, across pieces
+            w.init(p, bars, work);
+            int issued = 0, left_q = 0;     // QKs issued; tiles left of their piece
+            int kst = 0, qb = 0, qs = 1;    // K stage, S buffer and Q slot of the next QK
+            uint32_t kpar = 0, qpar = 1;    // phase parities of K stage and Q slot
+            uint32_t ends = 0;              // bit i: tile jj + i is the last of its piece
+            bool q_here = false;            // the piece's Q has landed
+            int jj = 0, st = 0, b = 0;      // PVs issued; V stage and S buffer of the next one
+            uint32_t vpar = 0, ppar = 0, opar = 1;
+            bool first = true;              // the next PV is the first of its piece
+            bool ok = true;
+            for (;;) {
+                // S(t mod 3) is free for QK(t + 3) once PV(t) is issued.  QK(jj)
+                // must be on its way before P(jj) is awaited; later QKs go now
+                // only if their operands have landed, so that a late K never
+                // holds back the next PV.
+                while (issued < min(jj + 3, quota)) {
                     if (left_q == 0) {
-                        if (!wq.next(p, pq)) return false;
-                        ++nq;
-                        left_q = -pq.nt;  // negative: the piece's Q has not been waited for
+                        Piece pq;
+                        w.next(p, pq);
+                        left_q = pq.nt;
+                        qs ^= 1;
+                        if (qs == 0) qpar ^= 1;
+                        q_here = false;
                     }
-                    const int st = issued % KS;
-                    const uint32_t par = (issued / KS) & 1;
-                    if (block) {
-                        if ((left_q < 0 && !mbar_wait_warp(&bars->q_full[nq & 1], (nq >> 1) & 1, p.err, abort)) ||
-                            !mbar_wait_warp(&bars->k_full[st], par, p.err, abort)) {
-                            ok = false;
-                            return false;
-                        }
-                    } else if ((left_q < 0 &&
-                                !__all_sync(0xFFFFFFFFu, mbar_try_wait(&bars->q_full[nq & 1], (nq >> 1) & 1))) ||
-                               !__all_sync(0xFFFFFFFFu, mbar_try_wait(&bars->k_full[st], par))) {
-                        return false;
-                    }
-                    if (left_q < 0) left_q = -left_q;
-                    tc_fence_after();
-                    issue_qk<D>(tmem + 128 * (issued % 3), dq0 + (nq & 1) * (SL::kQBytes >> 4), dk0 + st * (SL::kKHalf >> 4));
-                    commit_warp(&bars->s_full[issued % 3]);
-                    commit_warp(&bars->k_empty[st]);
-                    if (--left_q == 0) commit_warp(&bars->q_empty[nq & 1]);  // the piece's last QK
-                    ++issued;
-                    return true;
-                };
-                while (ok && issued < min(3, quota)) qk_next(true);
-                Piece pc;
-                int jj = 0, npc = 0;
-                while (ok && wv.next(p, pc)) {
-                    for (int j = 0; ok && j < pc.nt; ++j, ++jj) {
-                        const int st = jj % VS, b = jj % 3;
-                        ok = mbar_wait_warp(&bars->p_full[b], (jj / 3) & 1, p.err, abort) &&
-                             mbar_wait_warp(&bars->v_full[st], (jj / VS) & 1, p.err, abort);
-                        // the previous piece's O has been read out
-                        if (ok && j == 0 && npc > 0) ok = mbar_wait_warp(&bars->o_free, (npc - 1) & 1, p.err, abort);
+                    if (issued <= jj) {
+                        ok = (q_here || mbar_wait_warp(&bars->q_full[qs], qpar, p.err, abort)) &&
+                             mbar_wait_warp(&bars->k_full[kst], kpar, p.err, abort);
                         if (!ok) break;
-                        tc_fence_after();
-                        issue_pv<D>(tmem + 384, tmem + 128 * b, dv0 + st * (SL::kVHalf >> 4), j > 0);
-                        commit_warp(&bars->o_done[b]);
-                        commit_warp(&bars->v_empty[st]);
-                        // S(jj mod 3) is free for QK(jj + 3) once PV(jj) is issued.
-                        // QK(jj + 1) must be on its way before P(jj + 1) is awaited;
-                        // later QKs go now only if their operands have landed, so
-                        // that a late K never holds back the next PV
-                        while (ok && issued < min(jj + 4, quota))
-                            if (!qk_next(issued <= jj + 1)) break;
+                    } else if (!(q_here || __all_sync(0xFFFFFFFFu, mbar_try_wait(&bars->q_full[qs], qpar))) ||
+                               !__all_sync(0xFFFFFFFFu, mbar_try_wait(&bars->k_full[kst], kpar))) {
+                        break;
                     }
-                    ++npc;
+                    q_here = true;
+                    --left_q;
+                    tc_fence_after();
+                    issue_qk<D>(tmem + 128 * qb, dq0 + qs * (SL::kQBytes >> 4), dk0 + kst * (SL::kKHalf >> 4),
+                                &bars->s_full[qb], &bars->k_empty[kst], left_q == 0 ? &bars->q_empty[qs] : nullptr);
+                    if (left_q == 0) ends |= 1u << (issued - jj);
+                    ++issued;
+                    if (++kst == KS) kst = 0, kpar ^= 1;
+                    if (++qb == 3) qb = 0;
                 }
-                commit_warp(&bars->mma_final);
+                if (!ok || jj == quota) break;
+                ok = mbar_wait_warp(&bars->v_full[st], vpar, p.err, abort);
+                // the previous piece's O has been read out
+                if (ok && first && jj > 0) ok = mbar_wait_warp(&bars->o_free, opar, p.err, abort);
+                ok = ok && mbar_wait_warp(&bars->p_full[b], ppar, p.err, abort);
+                if (!ok) break;
+                tc_fence_after();
+                issue_pv<D>(tmem + 384, tmem + 128 * b, dv0 + st * (SL::kVHalf >> 4), !first, &bars->o_done[b],
+                            &bars->v_empty[st]);
+                first = ends & 1u;
+                if (first) opar ^= 1;
+                ends >>= 1;
+                ++jj;
+                if (++st == VS) st = 0, vpar ^= 1;
+                if (++b == 3) b = 0, ppar ^= 1;
             }
+            commit_warp(&bars->mma_final);
         }
     } else if (quota > 0) {
         // ------------------------------------------------------- softmax
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
         const int x = static_cast<int>(rank);
         const int wg = warp >> 2, w4 = warp & 3;
         const int r = tid & 127;  // query row = TMEM lane
@@ -941,116 +963,114 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         float2* xch = reinterpret_cast<float2*>(smem + SL::kX) + w4 * 128;
         const uint32_t lead_p = cluster_map(&bars->p_full[0], 0);
         const uint32_t lead_free = cluster_map(&bars->o_free, 0);
-        Walker w;
-        w.init(p, bars, work);
-        Piece pc;
-        int cnt = 0, npc = 0;               // tiles and pieces so far
-        uint32_t mph = 0, own_seen = 0, own_par = 0;  // m_bar phase parities per tile parity; v_own phases
+        WarpWalk* ws = reinterpret_cast<WarpWalk*>(smem + SL::kW) + warp;
+        if (lane == 0) ws->w.init(p, bars, work);
+        int cnt = 0, npc = 0, fin = 0;      // tiles, pieces and unit-final tiles so far
         auto meet8 = [&](int i) -> bool {   // meeting i of a merge (a merge meets twice: parity i)
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars->msync);
             return mbar_wait_warp(&bars->msync, static_cast<uint32_t>(i), p.err, abort);
         };
-        // the partner warp has decided on the maxima after tile t - 1 / this one has after tile t
+        // the partner warp has decided on its maxima after tile t
         auto partner_done = [&](int t) -> bool {
-            const int o = (t - 1) & 1;
-            return mbar_wait_warp(&bars->m_bar[w4][o], ((mph >> o) & 1u) ^ 1u, p.err, abort);
+            return mbar_wait_warp(&bars->m_bar[w4][t & 1], (t >> 1) & 1, p.err, abort);
         };
         auto tell_partner = [&](int t) {
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars->m_bar[w4][t & 1]);
-            mph ^= 1u << (t & 1);
         };
         bool ok = true;
-        while (ok && w.next(p, pc)) {
-            const bool tile_on = (2 * pc.mp + x) * npt < pc.s.B;  // this CTA's query tile exists
-            const int L = pc.s.L;
+        while (ok) {
+            __syncwarp();
+            int more = 0;
+            if (lane == 0) more = ws->w.next(p, ws->pc) ? 1 : 0;
+            more = __shfl_sync(0xFFFFFFFFu, more, 0);
+            if (!more) break;
+            const Piece& pc = ws->pc;
             const int tok0 = (2 * pc.mp + x) * npt;
             const int token = tok0 + r / p.G;
-            const int head = pc.g * p.G + r % p.G;
             const bool valid_row = r < npt * p.G && token < pc.s.B;
             const bool warp_on = __any_sync(0xFFFFFFFFu, valid_row);
-            const int first_masked = L + tok0 + 1;  // tiles that end before this slot need no mask
+            const int nt = pc.nt;
+            const int visible0 = pc.s.L + token + 1 - pc.t0 * kTileN;  // keys of the row from the piece's first on
+            const int jdiag = (pc.s.L + tok0 + 1) / kTileN - pc.t0;    // tiles before it need no mask
+            const int jfin = pc.T - 1 - pc.t0;                         // the unit's final tile
             float m_run = -INFINITY, l_run = 0.0f;
-            for (int j = 0; j < pc.nt; ++j, ++cnt) {
-                const int b = cnt % 3;
-                if ((cnt & 1) != wg) {
-                    mph ^= 1u << (cnt & 1);  // the other warpgroup's tile: one more phase of its m_bar
-                    continue;
-                }
-                if (!mbar_wait_warp(&bars->s_full[b], (cnt / 3) & 1, p.err, abort)) {
+            for (int j = (cnt + wg) & 1; j < nt; j += 2) {
+                const int t = cnt + j, b = t % 3;
+                if (!mbar_wait_warp(&bars->s_full[b], (t / 3) & 1, p.err, abort)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
                 if (warp_on) {
                     const uint32_t tS = tmem + 128 * b + lane_off;
-                    const int slot0 = (pc.t0 + j) * kTileN;
-                    SRow sr;
-                    load_srow(tS, sr);
-                    if (slot0 + kTileN > first_masked) mask_srow(sr, L + token + 1 - slot0);
-                    const float mx_s = max_srow(sr) * sl2;
-                    if (j > 0 && !partner_done(cnt)) {
-                        ok = false;
-                        break;
-                    }
-                    // the row's maximum after the tile before, from the partner warp
-                    const float m_prev = j > 0 ? mbuf[((cnt - 1) & 1) * 128 + r] : -INFINITY;
-                    float m_new = m_prev, factor = 1.0f;
-                    bool resc = false;
-                    if (mx_s > m_prev + kRescaleLog2 || m_prev == -INFINITY) {
-                        m_new = fmaxf(m_prev, mx_s);
-                        resc = m_prev != -INFINITY && valid_row;
-                        if (resc) factor = ex2_approx(m_prev - m_new);
-                    }
-                    mbuf[(cnt & 1) * 128 + r] = m_new;
-                    tell_partner(cnt);
-                    if (m_new != m_run) {  // this warp's part of the sum follows
-                        l_run = m_run == -INFINITY ? 0.0f : l_run * ex2_approx(m_run - m_new);
-                        m_run = m_new;
-                    }
-                    // P = exp2(s*scale*log2e - m), written over S (bf16 pairs)
-                    l_run += exp_store_srow(sr, tS, sl2, m_run == -INFINITY ? 0.0f : m_run);
-                    if (__any_sync(0xFFFFFFFFu, resc)) {
-                        // O holds PV(cnt - 1) before it is rescaled
-                        if (!mbar_wait_warp(&bars->o_done[(cnt - 1) % 3], ((cnt - 1) / 3) & 1, p.err, abort)) {
+                    const bool diag = j >= jdiag;
+                    const int visible = visible0 - j * kTileN;
+                    const float mx_s = row_max(tS, diag, visible) * sl2;
+                    const float m_before = m_run;
+                    if (j == 1) {  // the row's first maximum, from the partner warp
+                        if (!partner_done(t - 1)) {
                             ok = false;
                             break;
                         }
-                        tc_fence_after();
-#pragma unroll 1
-                        for (int q = 0; q < D / 32; ++q) {
-                            uint32_t v[32];
-                            tmem_ld32(tO + q * 32, v);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) * factor);
-                            tmem_st32(tO + q * 32, v);
-                        }
+                        m_run = mbuf[((t - 1) & 1) * 128 + r];
                     }
+                    if (mx_s > m_run + kRescaleLog2 || m_run == -INFINITY) m_run = fmaxf(m_run, mx_s);
+                    // P = exp2(s*scale*log2e - m), written over S (bf16 pairs)
+                    float sum = row_exp(tS, diag, visible, sl2, m_run == -INFINITY ? 0.0f : m_run);
+                    float m_o = -INFINITY;  // what O is scaled by: the partner's m after the tile before
+                    if (j > 0) {
+                        if (!partner_done(t - 1)) {
+                            ok = false;
+                            break;
+                        }
+                        m_o = mbuf[((t - 1) & 1) * 128 + r];
+                    }
+                    const bool lag = m_o > m_run;                        // the partner has raised m: P follows
+                    const bool raise = m_run > m_o && m_o != -INFINITY;  // this tile raises it: O follows
+                    if (__any_sync(0xFFFFFFFFu, valid_row && (lag || raise))) {
+                        tmem_wait_st();
+                        if (__any_sync(0xFFFFFFFFu, valid_row && raise)) {
+                            // O holds PV(t - 1) before it is rescaled
+                            if (!mbar_wait_warp(&bars->o_done[(t - 1) % 3], ((t - 1) / 3) & 1, p.err, abort)) {
+                                ok = false;
+                                break;
+                            }
+                            tc_fence_after();
+                            scale_tmem<false>(tO, D / 32, raise ? ex2_approx(m_o - m_run) : 1.0f);
+                        }
+                        const float f = lag ? (m_run == -INFINITY ? 0.0f : ex2_approx(m_run - m_o)) : 1.0f;
+                        scale_tmem<true>(tS, 2, f);
+                        sum *= f;
+                        if (lag) m_run = m_o;
+                    }
+                    mbuf[(t & 1) * 128 + r] = m_run;
+                    tell_partner(t);
+                    if (m_before != m_run) l_run = m_before == -INFINITY ? 0.0f : l_run * ex2_approx(m_before - m_run);
+                    l_run += sum;
                     tmem_wait_st();
                 } else {
                     // Warps without rows keep step all the same: a warp waits
                     // only for its own tiles' S, and what it has seen of its
                     // partner covers the phases in between.
-                    if (j > 0 && !partner_done(cnt)) {
+                    if (j > 0 && !partner_done(t - 1)) {
                         ok = false;
                         break;
                     }
-                    tell_partner(cnt);
+                    tell_partner(t);
                 }
-                if (pc.t0 + j == pc.T - 1 && w4 == 0) {
+                if (j == jfin && w4 == 0) {
                     // the unit's final tile: zero the rows of its last page past the last needed slot
-                    const int st = cnt % VS;
-                    const uint32_t par = (own_seen >> st & 1u) ? (own_par >> st & 1u) ^ 1u : 0u;
-                    if (!mbar_wait_warp(&bars->v_own[st], par, p.err, abort)) {
+                    if (!mbar_wait_warp(&bars->v_own[fin % VS], (fin / VS) & 1, p.err, abort)) {
                         ok = false;
                         break;
                     }
                     const int nvalid = unit_end(pc.s, pc.mp, npt) - (pc.t0 + j) * kTileN;
                     const int end = (nvalid + JT_PAGE_SIZE - 1) / JT_PAGE_SIZE * JT_PAGE_SIZE;
                     for (int i = lane; i < (end - nvalid) * (SL::kVRow / 16); i += 32)
-                        reinterpret_cast<uint4*>(sV + st * SL::kVHalf + nvalid * SL::kVRow)[i] = make_uint4(0u, 0u, 0u, 0u);
+                        reinterpret_cast<uint4*>(sV + (t % VS) * SL::kVHalf + nvalid * SL::kVRow)[i] =
+                            make_uint4(0u, 0u, 0u, 0u);
                     fence_proxy_async_smem();
                 }
                 tc_fence_before();
@@ -1058,12 +1078,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (lane == 0) mbar_arrive_cluster(lead_p + 8 * b);
             }
             if (!ok) break;
-            if (pc.t0 + pc.nt == pc.T) {  // the unit's final tile used one more phase of its v_own
-                const int st = (cnt - 1) % VS;
-                own_par = (own_seen >> st & 1u) ? own_par ^ (1u << st) : own_par & ~(1u << st);
-                own_seen |= 1u << st;
-            }
-            if (w.remaining <= 0) pdl_trigger();
+            cnt += nt;
+            fin += jfin < nt ? 1 : 0;
+            if (ws->w.remaining <= 0) pdl_trigger();
             // ------------------------------------------- end of the piece
             // both warps of the rows: whole maxima and sums
             float2* xp = xch + (npc & 1) * 64;
@@ -1084,6 +1101,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 break;
             }
             tc_fence_after();
+            const bool tile_on = tok0 < pc.s.B;  // this CTA's query tile exists
             const bool partial = pc.slot >= 0;
             uint32_t v[kHalfCols / 32][32];
             if (warp_on) {
@@ -1095,7 +1113,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(lead_free);
-            const long long rowid = static_cast<long long>(pc.s.off + token) * p.Hq + head;
+            const long long rowid = static_cast<long long>(pc.s.off + token) * p.Hq + pc.g * p.G + r % p.G;
             if (warp_on && partial) {
                 const long long prow = (static_cast<long long>(pc.slot) * 2 + x) * kTileM + r;
 #pragma unroll
@@ -1141,7 +1159,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     const int rr = __ffs(bad) - 1;
                     bad &= bad - 1;
                     __syncwarp();
-                    redo_row<D, kHalfCols / 32>(p, pc.b, L, pc.g, __shfl_sync(0xFFFFFFFFu, token, rr),
+                    redo_row<D, kHalfCols / 32>(p, pc.b, pc.s.L, pc.g, __shfl_sync(0xFFFFFFFFu, token, rr),
                                                 __shfl_sync(0xFFFFFFFFu, rowid, rr), wg * kHalfCols, lane);
                 }
             }
