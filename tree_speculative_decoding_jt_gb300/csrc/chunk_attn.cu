@@ -24,23 +24,25 @@
 // number of tiles.  A unit cut by a range boundary leaves fp32 partials; the
 // slot that finishes its last piece merges them, summing in piece order.
 //
-// Warps per CTA (384 threads; warp 11 idles):
+// Warps per CTA (512 threads; warp 15 idles):
 //   0-3 / 4-7  softmax of the tiles with even / odd number, one query row per
 //              thread.  Warps w and w + 4 hold the same 32 rows, and each warp
 //              has two tiles' time for one tile's softmax.  P of all tiles of a
-//              row is relative to one maximum m: each warp keeps the largest it
-//              knows, tells the other after every tile (m_bar) and its own part
-//              of the sum.  m is the first tile's maximum, raised only when a
-//              later score exceeds it by 2^32: P, O and l then stay far inside
-//              fp32, with no loss of relative precision, and the partner's m is
-//              not on the way of a tile's exponentials.  Warps whose rows are
-//              all past the chunk's end (single tokens fill 1 to 16 of 256 rows)
-//              compute nothing.
-//   8 / 10     TMA producers of Q and K / of V, one box per 16-token page;
-//   9          TMEM allocation; in the pair's leader, the MMA issuer.
+//              row is relative to one maximum m: each warp keeps the m it knows
+//              and its own part of the sum, and tells the other m after every
+//              tile.  m is the first tile's maximum, raised only when a later
+//              score exceeds it by 2^32: P, O and l then stay far inside fp32,
+//              with no loss of relative precision, and the partner's m is not on
+//              the way of a tile's exponentials.  Warps whose rows are all past
+//              the chunk's end (single tokens fill 1 to 16 of 256 rows) compute
+//              nothing.
+//   8-11       epilogue: O of a piece to the output or to its partial, and the
+//              merges, while the softmax warps are at the next piece's tiles;
+//   12 / 14    TMA producers of Q and K / of V, one box per 16-token page;
+//   13         TMEM allocation; in the pair's leader, the MMA issuer.
 // TMEM (512 columns): S0, S1, S2 (P of a tile overwrites the first half of its
-// S) and O.  The products S run up to three tiles ahead of O's, across units;
-// Q is double buffered.
+// S) and O.  The MMA warp issues QK up to three tiles ahead, across units; Q is
+// double buffered.
 #include <algorithm>
 
 #include "jt_common.cuh"
@@ -49,7 +51,11 @@
 namespace jt {
 namespace chunk {
 
-constexpr int kThreads = 384;
+constexpr int kThreads = 512;
+// Registers: 128 a thread at launch; the softmax and epilogue warps take what
+// the others give up: 256 * 136 + 128 * 160 + 128 * 80 = 512 * 128.
+constexpr int kSoftmaxRegs = 136, kEpilogueRegs = 160, kOtherRegs = 80;
+constexpr int kRing = 4;     // pieces whose rows' sums may wait for the epilogue
 constexpr int kTileN = 128;  // keys per KV tile
 constexpr int kTileM = 128;  // query rows per query tile
 constexpr float kRescaleLog2 = 32.0f;
@@ -86,12 +92,12 @@ struct Smem {
     static constexpr int kQ = 0;                            // two Q tiles
     static constexpr int kK = kQ + 2 * kQBytes;
     static constexpr int kV = kK + kKStages * kKHalf;
-    static constexpr int kStage = kV + kVStages * kVHalf;   // epilogue staging, 2 KB per softmax warp
-    static constexpr int kBar = kStage + 8 * 2048;
-    static constexpr int kM = kBar + 512;                   // running maxima [tile parity][row]
-    static constexpr int kX = kM + 1024;                    // (max, sum) [row / 32][piece parity][warpgroup][lane]
-    static constexpr int kW = kX + 4096;                    // the softmax warps' walks
-    static constexpr int kBytes = kW + 1024;
+    static constexpr int kStage = kV + kVStages * kVHalf;   // epilogue staging, 2 KB per warp
+    static constexpr int kBar = kStage + 4 * 2048;
+    static constexpr int kM = kBar + 1024;                  // [tile / 2 mod 2][warpgroup][row]: (tile + 1, maximum)
+    static constexpr int kX = kM + 4096;                    // [piece mod kRing][warpgroup][row]: (maximum, sum)
+    static constexpr int kW = kX + kRing * 2048;            // the softmax and epilogue warps' walks
+    static constexpr int kBytes = kW + 2048;
     static constexpr int kAlloc = kBytes + 1024;            // room to align the base to 1024
 };
 
@@ -108,18 +114,17 @@ struct Bars {
     uint64_t s_full[3];             // S buffer holds QK of its latest tile
     uint64_t p_full[3];             // leader: P of the tile in the S buffer, from 8 softmax warps
     uint64_t o_done[3];             // one phase per PV of a tile t with t mod 3 == index
-    uint64_t o_free;                // leader: the pair's 16 softmax warps have read the piece's O
+    uint64_t o_free;                // leader: the pair's 8 epilogue warps have read the piece's O
     uint64_t mma_final;             // every MMA of the pair has completed
-    uint64_t m_bar[4][2];           // warps w, w + 4: the running maxima after a tile of this parity
-    uint64_t x_bar[4];              // warps w, w + 4 meet at the end of a piece
-    uint64_t msync;                 // this CTA's 8 softmax warps meet (merge of a cut unit)
+    uint64_t x_bar[kRing][4];       // warps w, w + 4 have left a piece's maxima and sums for the epilogue
+    uint64_t msync;                 // this CTA's 4 epilogue warps meet (merge of a cut unit)
     uint32_t tmem_base;
     int abort;
     int w_b, w_g, w_mp, w_t, w_quota, w_P;
     uint32_t call_id;
     int merge_flag;
 };
-static_assert(sizeof(Bars) <= 512, "barrier block");
+static_assert(sizeof(Bars) <= 1024, "barrier block");
 
 // ---------------------------------------------------------------------------
 // The work plan
@@ -244,7 +249,7 @@ struct WarpWalk {
     Walker w;
     Piece pc;
 };
-static_assert(8 * sizeof(WarpWalk) <= 1024, "walk block");
+static_assert(12 * sizeof(WarpWalk) <= 2048, "walk block");
 
 __device__ __forceinline__ long long warp_sum(long long v) {
 #pragma unroll
@@ -443,6 +448,28 @@ __device__ __forceinline__ float row_exp(uint32_t tS, bool diag, int visible, fl
     return (a0 + a1) + (b0 + b1);
 }
 
+// The partner warp's word for tile t, (t + 1, m) (bounded: false when it gives
+// up, the error raised).
+__device__ __forceinline__ bool partner_max(volatile unsigned long long* word, int t, float& m, uint32_t* err,
+                                            volatile int* abort) {
+    unsigned long long t0 = 0ull;
+    for (uint32_t i = 1;; ++i) {
+        const unsigned long long v = *word;
+        m = __uint_as_float(static_cast<uint32_t>(v));
+        if (__all_sync(0xFFFFFFFFu, static_cast<uint32_t>(v >> 32) == static_cast<uint32_t>(t) + 1u)) return true;
+        if ((i & 63u) == 0u) {
+            if (__any_sync(0xFFFFFFFFu, *abort != 0)) return false;
+            const unsigned long long now = globaltimer_ns();
+            if (t0 == 0ull) t0 = now;
+            if (__any_sync(0xFFFFFFFFu, now - t0 > kWaitLimitNs)) {
+                raise_error(err, DEVERR_TIMEOUT);
+                *abort = 1;
+                return false;
+            }
+        }
+    }
+}
+
 // 32 * n columns of tensor memory times f (this thread's row): fp32, or bf16
 // pairs.  Out of line: it runs when a row's maximum has grown by more than 2^32.
 template <bool kPairs>
@@ -609,65 +636,78 @@ __device__ __forceinline__ int bt_group(const Params& p, const Piece& pc, int va
                : 0;
 }
 
-// Merge of a cut unit's pieces for this CTA's query tile x: rows are dealt to
-// the 8 softmax warps, four at a time.  Per row M = max m_k, O = sum_k
-// 2^(m_k - M) O_k / sum_k 2^(m_k - M) l_k, in piece order whoever merges, so
-// every call rounds the same way.
-template <int D>
+// Merge of a cut unit's pieces for this CTA's query tile x.  Rows are dealt to
+// the 4 epilogue warps, R at a time; per row M = max m_k, O = sum_k 2^(m_k - M)
+// O_k / sum_k 2^(m_k - M) l_k, in piece order whoever merges, so every call
+// rounds the same way.  R x K partial rows are in flight: many rows of few
+// pieces (prompts) or few rows of many (single tokens).
+template <int D, int R, int K>
 __device__ __noinline__ void merge_rows(const Params& p, const Piece& pc, const CutUnit cu, int x, int swarp,
                                         int lane) {
+    static_assert(R * K <= 32, "one (row, piece) per lane");
     constexpr int kC = D / 32;  // columns per lane
     const int tok0 = (2 * pc.mp + x) * p.npt;
     const int rows = min(pc.s.B - tok0, p.npt) * p.G;
-    const int sub = lane & 7, rsub = lane >> 3;  // lane = (row of the batch, piece of the group)
-    for (int r0 = swarp * 4; r0 < rows; r0 += 32) {
-        const int myr = min(r0 + rsub, rows - 1);
-        auto prow = [&](int k, int r) {
-            return (static_cast<long long>(cu.slot(k)) * 2 + x) * kTileM + r;
-        };
-        float M = -INFINITY;
-        for (int k = sub; k < cu.n; k += 8) M = fmaxf(M, __ldcg(&p.part_ml[prow(k, myr)]).x);
+    const int sub = lane % K, rsub = (lane / K) % R;  // lane = (row of the batch, piece of the group)
+    const long long stride = static_cast<long long>(2) * kTileM;  // between partial slots
+    for (int r0 = swarp * R; r0 < rows; r0 += 4 * R) {
+        const long long xr = static_cast<long long>(x) * kTileM + min(r0 + rsub, rows - 1);
+        float M[R], lsum[R], acc[R][kC];
 #pragma unroll
-        for (int o = 4; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
-        float acc[4][kC], lsum[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < R; ++i) {
+            M[i] = -INFINITY;
             lsum[i] = 0.0f;
 #pragma unroll
             for (int c = 0; c < kC; ++c) acc[i][c] = 0.0f;
         }
-        for (int k0 = 0; k0 < cu.n; k0 += 8) {
-            const float2 ml = k0 + sub < cu.n ? __ldcg(&p.part_ml[prow(k0 + sub, myr)]) : make_float2(-INFINITY, 0.0f);
-            const float w = ml.x == -INFINITY ? 0.0f : exp2f(ml.x - M);
-            const float wl = w * ml.y;
-            for (int k = 0; k < min(8, cu.n - k0); ++k) {
-                float v[4][kC];
+#pragma unroll 1
+        for (int k0 = 0; k0 < cu.n; k0 += K) {
+            const float2 ml = k0 + sub < cu.n ? __ldcg(&p.part_ml[cu.slot(k0 + sub) * stride + xr])
+                                              : make_float2(-INFINITY, 0.0f);
+            float v[R][K][kC];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float* src = p.part_o + prow(k0 + k, min(r0 + i, rows - 1)) * D + lane * kC;
-                    if (kC == 4) {
+            for (int i = 0; i < R; ++i)
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+                    const float* src = p.part_o +
+                                       (cu.slot(min(k0 + k, cu.n - 1)) * stride + x * kTileM + min(r0 + i, rows - 1)) * D +
+                                       lane * kC;
+                    if constexpr (kC == 4) {
                         const float4 f = __ldcg(reinterpret_cast<const float4*>(src));
-                        v[i][0] = f.x, v[i][1] = f.y, v[i][2 % kC] = f.z, v[i][3 % kC] = f.w;
+                        v[i][k][0] = f.x, v[i][k][1] = f.y, v[i][k][2] = f.z, v[i][k][3] = f.w;
                     } else {
                         const float2 f = __ldcg(reinterpret_cast<const float2*>(src));
-                        v[i][0] = f.x, v[i][1] = f.y;
+                        v[i][k][0] = f.x, v[i][k][1] = f.y;
                     }
                 }
+            float mx = ml.x;  // the group's maximum of this lane's row
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float wk = __shfl_sync(0xFFFFFFFFu, w, 8 * i + k);
-                    lsum[i] += __shfl_sync(0xFFFFFFFFu, wl, 8 * i + k);
-                    // a piece without a visible key has weight 0, and O that nothing wrote to
-                    if (wk != 0.0f)
+            for (int o = K / 2; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
 #pragma unroll
-                        for (int c = 0; c < kC; ++c) acc[i][c] += wk * v[i][c];
+            for (int i = 0; i < R; ++i) {
+                const float mi = fmaxf(M[i], __shfl_sync(0xFFFFFFFFu, mx, i * K));
+                const float old = M[i] == -INFINITY ? 0.0f : exp2f(M[i] - mi);  // what earlier groups are worth now
+                M[i] = mi;
+                lsum[i] *= old;
+#pragma unroll
+                for (int c = 0; c < kC; ++c) acc[i][c] *= old;
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+                    const float mk = __shfl_sync(0xFFFFFFFFu, ml.x, i * K + k);
+                    const float lk = __shfl_sync(0xFFFFFFFFu, ml.y, i * K + k);
+                    // a piece without a visible key has weight 0, and O that says nothing
+                    if (mk != -INFINITY) {
+                        const float w = exp2f(mk - mi);
+                        lsum[i] += w * lk;
+#pragma unroll
+                        for (int c = 0; c < kC; ++c) acc[i][c] += w * v[i][k][c];
+                    }
                 }
             }
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < R; ++i) {
             const int r = r0 + i;
-            const float Mi = __shfl_sync(0xFFFFFFFFu, M, 8 * i);
             if (r >= rows) continue;
             const int token = tok0 + r / p.G;
             const long long rowid = static_cast<long long>(pc.s.off + token) * p.Hq + pc.g * p.G + r % p.G;
@@ -679,11 +719,11 @@ __device__ __noinline__ void merge_rows(const Params& p, const Piece& pc, const 
                 probe += o[c] * 0.0f;
             }
             __nv_bfloat16* dst = p.out + rowid * D + lane * kC;
-            if (kC == 4)
-                *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2 % kC], o[3 % kC]));
+            if constexpr (kC == 4)
+                *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
             else
                 *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(o[0], o[1]);
-            if (lane == 0 && p.lse) p.lse[rowid] = (Mi + log2f(lsum[i])) * 0.6931471805599453f;
+            if (lane == 0 && p.lse) p.lse[rowid] = (M[i] + log2f(lsum[i])) * 0.6931471805599453f;
             if (lsum[i] == lsum[i] && __any_sync(0xFFFFFFFFu, probe != 0.0f)) {
                 __syncwarp();
                 redo_row<D, kC>(p, pc.b, pc.s.L, pc.g, token, rowid, 0, lane);
@@ -698,7 +738,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                       const __grid_constant__ CUtensorMap tm_v, const Params p) {
     using SL = Smem<D>;
     constexpr int KS = SL::kKStages, VS = SL::kVStages;
-    constexpr int kHalfCols = D / 2;  // output columns per softmax warpgroup
+    constexpr int kHalfCols = D / 2;  // dims of V per CTA
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -724,23 +764,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             mbar_init(&bars->p_full[x], 8);
             mbar_init(&bars->o_done[x], 1);
         }
-        mbar_init(&bars->o_free, 16);
+        mbar_init(&bars->o_free, 8);
         mbar_init(&bars->mma_final, 1);
-        for (int w = 0; w < 4; ++w) {
-            mbar_init(&bars->m_bar[w][0], 1);
-            mbar_init(&bars->m_bar[w][1], 1);
-            mbar_init(&bars->x_bar[w], 2);
-        }
-        mbar_init(&bars->msync, 8);
+        for (int i = 0; i < kRing; ++i)
+            for (int w = 0; w < 4; ++w) mbar_init(&bars->x_bar[i][w], 2);
+        mbar_init(&bars->msync, 4);
         bars->abort = 0;
         fence_mbar_init();
     }
-    if (warp == 8 && lane == 0) {
+    if (warp == 12 && lane == 0) {
         tma_prefetch_desc(&tm_q);
         tma_prefetch_desc(&tm_k);
         tma_prefetch_desc(&tm_v);
     }
-    if (warp == 9) tmem_alloc_pair(&bars->tmem_base, 512);
+    if (warp == 13) tmem_alloc_pair(&bars->tmem_base, 512);
     // The V ring starts as zeros, and the rows of a unit-final tile's last page
     // past the needed slots are zeroed once it has landed: rows that no copy of
     // the present tile wrote are then always finite (P is 0 there, but 0 * NaN
@@ -748,9 +785,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (int i = tid; i < VS * SL::kVHalf / 16; i += kThreads)
         reinterpret_cast<uint4*>(smem + SL::kV)[i] = make_uint4(0u, 0u, 0u, 0u);
     fence_proxy_async_smem();
+    reinterpret_cast<uint64_t*>(smem + SL::kM)[tid] = 0ull;  // kThreads words: no tile yet
     cluster_sync();  // both CTAs' barriers exist before any copy, commit or arrive crosses the pair
     pdl_wait();      // no global memory is read before the previous kernel's writes are visible
-    if (warp == 8) plan_slot(p, bars, lane, work, nwork, work == 0 && rank == 0);
+    if (warp == 12) plan_slot(p, bars, lane, work, nwork, work == 0 && rank == 0);
     if (tid == 0) bars->call_id = draw_call_id(p.tickets, work == 0 && rank == 0, gridDim.x);
     tc_fence_before();
     __syncthreads();
@@ -764,8 +802,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint8_t* sV = smem + SL::kV;
     const int npt = p.npt;
 
-    if (quota > 0 && warp >= 8) {
-        if (warp == 8) {
+    if (quota > 0 && warp >= 12) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        if (warp == 12) {
             // ------------------------------------------------------- TMA: Q, K
             Walker w;
             w.init(p, bars, work);
@@ -820,7 +859,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     mbar_wait(&bars->k_full[j % KS], (j / KS) & 1, p.err, nullptr);
                 for (int n = max(0, npc - 2); n < npc; ++n) mbar_wait(&bars->q_full[n & 1], (n >> 1) & 1, p.err, nullptr);
             }
-        } else if (warp == 10) {
+        } else if (warp == 14) {
             // ---------------------------------------------------------- TMA: V
             Walker w;
             w.init(p, bars, work);
@@ -880,7 +919,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     for (int j = max(0, jj - VS); j < jj; ++j)
                         mbar_wait(&bars->v_full[j % VS], (j / VS) & 1, p.err, nullptr);
             }
-        } else if (rank == 0 && warp == 9) {
+        } else if (rank == 0 && warp == 13) {
             // -------------------------------------------------------- MMA
             // One thread issues both products, in an order that the tensor
             // pipe then keeps: QK(t + 3) right behind PV(t), which frees its S
@@ -950,35 +989,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             commit_warp(&bars->mma_final);
         }
-    } else if (quota > 0) {
+    } else if (quota > 0 && warp < 8) {
         // ------------------------------------------------------- softmax
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
         const int x = static_cast<int>(rank);
         const int wg = warp >> 2, w4 = warp & 3;
         const int r = tid & 127;  // query row = TMEM lane
         const uint32_t lane_off = static_cast<uint32_t>(w4 * 32) << 16;
         const uint32_t tO = tmem + 384 + lane_off;
         const float sl2 = p.scale_log2;
-        uint8_t* stage = smem + SL::kStage + warp * 2048;
-        volatile float* mbuf = reinterpret_cast<volatile float*>(smem + SL::kM);
-        float2* xch = reinterpret_cast<float2*>(smem + SL::kX) + w4 * 128;
+        // The two warps of a row tell each other its m after every tile, lane
+        // to lane in one 8-byte word.  A warp writes the word of tile t + 4 over
+        // that of tile t, which its partner has read by then: each waits for the
+        // other's word of the tile before in every tile.
+        volatile unsigned long long* words = reinterpret_cast<volatile unsigned long long*>(smem + SL::kM) + r;
+        auto word_of = [&](int t) { return words + ((t >> 1 & 1) * 2 + (t & 1)) * 128; };
+        auto tell_partner = [&](int t, float m) {
+            *word_of(t) = static_cast<unsigned long long>(t + 1) << 32 | __float_as_uint(m);
+        };
+        float2* xch = reinterpret_cast<float2*>(smem + SL::kX) + wg * 128 + r;
         const uint32_t lead_p = cluster_map(&bars->p_full[0], 0);
-        const uint32_t lead_free = cluster_map(&bars->o_free, 0);
         WarpWalk* ws = reinterpret_cast<WarpWalk*>(smem + SL::kW) + warp;
         if (lane == 0) ws->w.init(p, bars, work);
         int cnt = 0, npc = 0, fin = 0;      // tiles, pieces and unit-final tiles so far
-        auto meet8 = [&](int i) -> bool {   // meeting i of a merge (a merge meets twice: parity i)
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars->msync);
-            return mbar_wait_warp(&bars->msync, static_cast<uint32_t>(i), p.err, abort);
-        };
-        // the partner warp has decided on its maxima after tile t
-        auto partner_done = [&](int t) -> bool {
-            return mbar_wait_warp(&bars->m_bar[w4][t & 1], (t >> 1) & 1, p.err, abort);
-        };
-        auto tell_partner = [&](int t) {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars->m_bar[w4][t & 1]);
-        };
         bool ok = true;
         while (ok) {
             __syncwarp();
@@ -1003,62 +1036,63 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     break;
                 }
                 tc_fence_after();
+                // Warps without rows keep step all the same: a warp waits only
+                // for its own tiles' S, and the partner's words tell it that the
+                // phases in between have passed.
+                float m_o = -INFINITY;  // the partner's m after the tile before: what O is scaled by
                 if (warp_on) {
                     const uint32_t tS = tmem + 128 * b + lane_off;
                     const bool diag = j >= jdiag;
                     const int visible = visible0 - j * kTileN;
                     const float mx_s = row_max(tS, diag, visible) * sl2;
                     const float m_before = m_run;
-                    if (j == 1) {  // the row's first maximum, from the partner warp
-                        if (!partner_done(t - 1)) {
+                    if (j < 2 && t > 0) {
+                        // j = 1: the row's first maximum; j = 0: the word to be
+                        // written next may still be unread before this
+                        if (!partner_max(word_of(t - 1), t - 1, m_o, p.err, abort)) {
                             ok = false;
                             break;
                         }
-                        m_run = mbuf[((t - 1) & 1) * 128 + r];
+                        if (j == 1) m_run = m_o;
                     }
                     if (mx_s > m_run + kRescaleLog2 || m_run == -INFINITY) m_run = fmaxf(m_run, mx_s);
+                    if (j == 0) tell_partner(t, m_run);  // early: the partner's first tile waits for it
                     // P = exp2(s*scale*log2e - m), written over S (bf16 pairs)
                     float sum = row_exp(tS, diag, visible, sl2, m_run == -INFINITY ? 0.0f : m_run);
-                    float m_o = -INFINITY;  // what O is scaled by: the partner's m after the tile before
                     if (j > 0) {
-                        if (!partner_done(t - 1)) {
+                        if (j > 1 && !partner_max(word_of(t - 1), t - 1, m_o, p.err, abort)) {
                             ok = false;
                             break;
                         }
-                        m_o = mbuf[((t - 1) & 1) * 128 + r];
-                    }
-                    const bool lag = m_o > m_run;                        // the partner has raised m: P follows
-                    const bool raise = m_run > m_o && m_o != -INFINITY;  // this tile raises it: O follows
-                    if (__any_sync(0xFFFFFFFFu, valid_row && (lag || raise))) {
-                        tmem_wait_st();
-                        if (__any_sync(0xFFFFFFFFu, valid_row && raise)) {
-                            // O holds PV(t - 1) before it is rescaled
-                            if (!mbar_wait_warp(&bars->o_done[(t - 1) % 3], ((t - 1) / 3) & 1, p.err, abort)) {
-                                ok = false;
-                                break;
+                        if (__any_sync(0xFFFFFFFFu, valid_row && m_o != m_run)) {
+                            const bool raise = m_run > m_o && m_o != -INFINITY;  // this tile raises m: O follows
+                            const bool lag = m_o > m_run;                        // the partner has raised it: P follows
+                            tmem_wait_st();
+                            if (__any_sync(0xFFFFFFFFu, valid_row && raise)) {
+                                // O holds PV(t - 1) before it is rescaled
+                                if (!mbar_wait_warp(&bars->o_done[(t - 1) % 3], ((t - 1) / 3) & 1, p.err, abort)) {
+                                    ok = false;
+                                    break;
+                                }
+                                tc_fence_after();
+                                scale_tmem<false>(tO, D / 32, raise ? ex2_approx(m_o - m_run) : 1.0f);
                             }
-                            tc_fence_after();
-                            scale_tmem<false>(tO, D / 32, raise ? ex2_approx(m_o - m_run) : 1.0f);
+                            const float f = lag ? (m_run == -INFINITY ? 0.0f : ex2_approx(m_run - m_o)) : 1.0f;
+                            scale_tmem<true>(tS, 2, f);
+                            sum *= f;
+                            if (lag) m_run = m_o;
                         }
-                        const float f = lag ? (m_run == -INFINITY ? 0.0f : ex2_approx(m_run - m_o)) : 1.0f;
-                        scale_tmem<true>(tS, 2, f);
-                        sum *= f;
-                        if (lag) m_run = m_o;
+                        tell_partner(t, m_run);
                     }
-                    mbuf[(t & 1) * 128 + r] = m_run;
-                    tell_partner(t);
                     if (m_before != m_run) l_run = m_before == -INFINITY ? 0.0f : l_run * ex2_approx(m_before - m_run);
                     l_run += sum;
                     tmem_wait_st();
                 } else {
-                    // Warps without rows keep step all the same: a warp waits
-                    // only for its own tiles' S, and what it has seen of its
-                    // partner covers the phases in between.
-                    if (j > 0 && !partner_done(t - 1)) {
+                    if (t > 0 && !partner_max(word_of(t - 1), t - 1, m_o, p.err, abort)) {
                         ok = false;
                         break;
                     }
-                    tell_partner(t);
+                    tell_partner(t, -INFINITY);
                 }
                 if (j == jfin && w4 == 0) {
                     // the unit's final tile: zero the rows of its last page past the last needed slot
@@ -1080,98 +1114,126 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (!ok) break;
             cnt += nt;
             fin += jfin < nt ? 1 : 0;
-            if (ws->w.remaining <= 0) pdl_trigger();
-            // ------------------------------------------- end of the piece
-            // both warps of the rows: whole maxima and sums
-            float2* xp = xch + (npc & 1) * 64;
-            xp[wg * 32 + lane] = make_float2(m_run, l_run);
+            // The rows' maxima and sums go to the epilogue.  Neither warpgroup is
+            // more than three pieces ahead of it: a tile's S waits for the PV
+            // three tiles before, and a piece's first PV for the epilogue.
+            xch[(npc % kRing) * 256] = make_float2(m_run, l_run);
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bars->x_bar[w4]);
-            if (!mbar_wait_warp(&bars->x_bar[w4], npc & 1, p.err, abort)) {
-                ok = false;
-                break;
-            }
-            const float2 xa = xp[lane], xb = xp[32 + lane];  // in this order for both warps
+            if (lane == 0) mbar_arrive(&bars->x_bar[npc % kRing][w4]);
+            ++npc;
+        }
+    } else if (quota > 0) {
+        // ------------------------------------------------------ epilogue
+        // one query row per thread, while the softmax warps go on to the next piece
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpilogueRegs));
+        const int x = static_cast<int>(rank);
+        const int w4 = warp & 3;
+        const int r = tid & 127;
+        const uint32_t tO = tmem + 384 + (static_cast<uint32_t>(w4 * 32) << 16);
+        uint8_t* stage = smem + SL::kStage + w4 * 2048;
+        const float2* xch = reinterpret_cast<const float2*>(smem + SL::kX) + r;
+        const uint32_t lead_free = cluster_map(&bars->o_free, 0);
+        WarpWalk* ws = reinterpret_cast<WarpWalk*>(smem + SL::kW) + warp;
+        if (lane == 0) ws->w.init(p, bars, work);
+        int last = -1, npc = 0;  // the piece's last tile; pieces so far
+        auto meet4 = [&](int i) -> bool {   // meeting i of a merge (a merge meets twice: parity i)
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->msync);
+            return mbar_wait_warp(&bars->msync, static_cast<uint32_t>(i), p.err, abort);
+        };
+        bool ok = true;
+        while (ok) {
+            __syncwarp();
+            int more = 0;
+            if (lane == 0) more = ws->w.next(p, ws->pc) ? 1 : 0;
+            more = __shfl_sync(0xFFFFFFFFu, more, 0);
+            if (!more) break;
+            const Piece& pc = ws->pc;
+            last += pc.nt;
+            const int tok0 = (2 * pc.mp + x) * npt;
+            const int token = tok0 + r / p.G;
+            const bool valid_row = r < npt * p.G && token < pc.s.B;
+            const bool warp_on = __any_sync(0xFFFFFFFFu, valid_row);
+            const bool tile_on = tok0 < pc.s.B;  // this CTA's query tile exists
+            const bool partial = pc.slot >= 0;
+            const long long rowid = static_cast<long long>(pc.s.off + token) * p.Hq + pc.g * p.G + r % p.G;
+            // both softmax warps of the rows are through the piece (so S of its last tile has been seen)
+            if (!mbar_wait_warp(&bars->x_bar[npc % kRing][w4], (npc / kRing) & 1, p.err, abort)) break;
+            const float2 xa = xch[(npc % kRing) * 256], xb = xch[(npc % kRing) * 256 + 128];
+            ++npc;
             const float m_tot = fmaxf(xa.x, xb.x);
             const float l_tot = (xa.x == -INFINITY ? 0.0f : xa.y * ex2_approx(xa.x - m_tot)) +
                                 (xb.x == -INFINITY ? 0.0f : xb.y * ex2_approx(xb.x - m_tot));
-            ++npc;
-            if (!mbar_wait_warp(&bars->o_done[(cnt - 1) % 3], ((cnt - 1) / 3) & 1, p.err, abort)) {
-                ok = false;
-                break;
-            }
+            if (ws->w.remaining <= 0) pdl_trigger();
+            if (!mbar_wait_warp(&bars->o_done[last % 3], (last / 3) & 1, p.err, abort)) break;
             tc_fence_after();
-            const bool tile_on = tok0 < pc.s.B;  // this CTA's query tile exists
-            const bool partial = pc.slot >= 0;
-            uint32_t v[kHalfCols / 32][32];
-            if (warp_on) {
+            if (warp_on && partial) {
+                const long long prow = (static_cast<long long>(pc.slot) * 2 + x) * kTileM + r;
+                float* dst = p.part_o + prow * D;
+#pragma unroll 1
+                for (int h = 0; h < D / 32; ++h) {
+                    uint32_t v[32];
+                    tmem_ld32(tO + 32 * h, v);
+                    tmem_wait_ld();
+                    if (valid_row)
 #pragma unroll
-                for (int h = 0; h < kHalfCols / 32; ++h) tmem_ld32(tO + wg * kHalfCols + 32 * h, v[h]);
-                tmem_wait_ld();
+                        for (int c = 0; c < 8; ++c)
+                            reinterpret_cast<uint4*>(dst + 32 * h)[c] =
+                                make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+                }
+                if (valid_row) p.part_ml[prow] = make_float2(m_tot, l_tot);
+            }
+            const float inv = 1.0f / l_tot;
+            float probe = 0.0f;
+            uint32_t packed[D / 2];
+            if (warp_on && !partial) {
+#pragma unroll
+                for (int h = 0; h < D / 32; ++h) {
+                    uint32_t v[32];
+                    tmem_ld32(tO + 32 * h, v);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) {
+                        const float a = __uint_as_float(v[2 * c]) * inv, b = __uint_as_float(v[2 * c + 1]) * inv;
+                        probe += a * 0.0f + b * 0.0f;
+                        packed[16 * h + c] = pack_bf16x2(a, b);
+                    }
+                }
             }
             // O has been read: the next piece's first PV may overwrite it
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(lead_free);
-            const long long rowid = static_cast<long long>(pc.s.off + token) * p.Hq + pc.g * p.G + r % p.G;
-            if (warp_on && partial) {
-                const long long prow = (static_cast<long long>(pc.slot) * 2 + x) * kTileM + r;
+            if (warp_on && !partial) {
 #pragma unroll
-                for (int h = 0; h < kHalfCols / 32; ++h) {
-                    uint4 slot[8];
-#pragma unroll
-                    for (int c = 0; c < 8; ++c)
-                        slot[c] = make_uint4(v[h][4 * c], v[h][4 * c + 1], v[h][4 * c + 2], v[h][4 * c + 3]);
-                    const int col = wg * kHalfCols + 32 * h;
-                    float* base = p.part_o + prow * D + col;
-                    if (valid_row)
-#pragma unroll
-                        for (int c = 0; c < 8; ++c) reinterpret_cast<uint4*>(base)[c] = slot[c];
-                }
-                if (wg == 0 && valid_row) p.part_ml[prow] = make_float2(m_tot, l_tot);
-            } else if (warp_on) {
-                const float inv = 1.0f / l_tot;
-                float probe = 0.0f;
-#pragma unroll
-                for (int h = 0; h < kHalfCols / 32; ++h) {
+                for (int h = 0; h < D / 32; ++h) {
                     uint4 slot[4];
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        float o[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            o[i] = __uint_as_float(v[h][8 * c + i]) * inv;
-                            probe += o[i] * 0.0f;
-                        }
-                        slot[c] = make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]),
-                                             pack_bf16x2(o[6], o[7]));
-                    }
-                    const int col = wg * kHalfCols + 32 * h;
+                    for (int c = 0; c < 4; ++c)
+                        slot[c] = make_uint4(packed[16 * h + 4 * c], packed[16 * h + 4 * c + 1],
+                                             packed[16 * h + 4 * c + 2], packed[16 * h + 4 * c + 3]);
                     stage_store<4>(stage, lane, slot, [&](int rr) {
                         const long long rid = __shfl_sync(0xFFFFFFFFu, rowid, rr);
                         const bool rvalid = __shfl_sync(0xFFFFFFFFu, valid_row, rr);
-                        return rvalid ? reinterpret_cast<uint4*>(p.out + rid * D + col) : nullptr;
+                        return rvalid ? reinterpret_cast<uint4*>(p.out + rid * D + 32 * h) : nullptr;
                     });
                 }
-                if (wg == 0 && valid_row && p.lse) p.lse[rowid] = (m_tot + log2f(l_tot)) * 0.6931471805599453f;
+                if (valid_row && p.lse) p.lse[rowid] = (m_tot + log2f(l_tot)) * 0.6931471805599453f;
                 unsigned bad = __ballot_sync(0xFFFFFFFFu, valid_row && probe != 0.0f && l_tot == l_tot);
                 while (bad) {
                     const int rr = __ffs(bad) - 1;
                     bad &= bad - 1;
                     __syncwarp();
-                    redo_row<D, kHalfCols / 32>(p, pc.b, pc.s.L, pc.g, __shfl_sync(0xFFFFFFFFu, token, rr),
-                                                __shfl_sync(0xFFFFFFFFu, rowid, rr), wg * kHalfCols, lane);
+                    redo_row<D, D / 32>(p, pc.b, pc.s.L, pc.g, __shfl_sync(0xFFFFFFFFu, token, rr),
+                                        __shfl_sync(0xFFFFFFFFu, rowid, rr), 0, lane);
                 }
             }
             if (partial && tile_on) {
                 // count this piece done; the slot that completes the unit merges every piece's rows
                 const CutUnit cu(pc.gpos - pc.t0, pc.T, bars->w_P);
-                __threadfence();  // this thread's partial rows are visible GPU-wide
-                if (!meet8(0)) {
-                    ok = false;
-                    break;
-                }
-                if (tid == 0) {
+                if (!meet4(0)) break;  // the warps' partial rows are written
+                if (w4 == 0 && lane == 0) {
+                    __threadfence();  // and visible GPU-wide before the count
                     const uint32_t cid = bars->call_id;
                     unsigned long long* ctr = p.merge_cnt + 2 * cu.c0 + x;
                     unsigned long long old = *reinterpret_cast<volatile unsigned long long*>(ctr), assumed, nv;
@@ -1184,11 +1246,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     bars->merge_flag = static_cast<int>(nv & 0xFFFFFFFFull) == cu.n;
                     __threadfence();  // the other pieces' rows are read after this count
                 }
-                if (!meet8(1)) {
-                    ok = false;
-                    break;
+                if (!meet4(1)) break;
+                if (bars->merge_flag) {
+                    if (cu.n <= 2)
+                        merge_rows<D, 8, 2>(p, pc, cu, x, w4, lane);
+                    else
+                        merge_rows<D, 2, 8>(p, pc, cu, x, w4, lane);
                 }
-                if (bars->merge_flag) merge_rows<D>(p, pc, cu, x, warp, lane);
             }
         }
     }
@@ -1196,9 +1260,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     // both CTAs: every MMA of the pair has completed before TMEM is released
-    if (warp == 9 && quota > 0) mbar_wait_warp(&bars->mma_final, 0, p.err, nullptr);
+    if (warp == 13 && quota > 0) mbar_wait_warp(&bars->mma_final, 0, p.err, nullptr);
     cluster_sync();  // no copy, arrive or MMA of the pair targets either CTA any more
-    if (warp == 9) {
+    if (warp == 13) {
         tc_fence_after();
         tmem_dealloc_pair(tmem, 512);
     }
