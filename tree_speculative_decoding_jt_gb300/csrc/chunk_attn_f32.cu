@@ -314,15 +314,18 @@ struct Plan {
     long long units;
 };
 
-// Keys are split when the units alone would leave half of the CTA slots (two
-// per SM) empty, at most one split per four key tiles.
+// Keys are split when the units (a dense count: shorter chunks leave some of
+// them empty) are fewer than eight rounds of the CTA slots, two per SM, at most
+// one split per four key tiles.  A key tile takes a CTA about 5 us, so a ragged
+// batch's longest unit sets the time: 4 sequences of 16 to 512 tokens over 128 to
+// 1500 (8/2 heads, D 64) took 204 us with splits for less than one round only.
 static Plan plan(int nseq, int Hq, int Hkv, int max_pages, int max_chunk) {
     Plan pl;
     pl.npt = std::max(1, kRows / (Hq / Hkv));
     pl.mtiles = (max_chunk + pl.npt - 1) / pl.npt;
     pl.units = static_cast<long long>(nseq) * Hkv * pl.mtiles;
     const long long tmax = (static_cast<long long>(max_pages) * JT_PAGE_SIZE + kKeys - 1) / kKeys;
-    const long long want = 2ll * std::max(1, device_sm_count()) / std::max(1ll, pl.units);
+    const long long want = 16ll * std::max(1, device_sm_count()) / std::max(1ll, pl.units);
     pl.splits = static_cast<int>(std::max(1ll, std::min({want, tmax / 4, static_cast<long long>(kMaxSplits)})));
     return pl;
 }

@@ -97,7 +97,33 @@ __global__ void __launch_bounds__(kAppendThreads) qkv_append_kernel(const Append
     const int lane = threadIdx.x & 31;
     const long long gw = static_cast<long long>(blockIdx.x) * (kAppendThreads / 32) + (threadIdx.x >> 5);
     const int i = static_cast<int>(gw / p.warps_per_token), part = static_cast<int>(gw % p.warps_per_token);
-    if (i >= p.total || i >= p.off[p.nseq]) return;
+    if (i >= p.total) return;
+    const int t = lane % LPH;
+    const bool on = kActive == LPH || t < kActive;
+    const int p0 = t * N;  // first of this lane's pairs
+    const bool rotated = on && p0 < p.rot / 2;
+    const bool split = rotated && !p.interleaved;
+    const int e0 = on ? (split ? p0 : 2 * p0) : 0, e1 = on ? (split ? p.rot / 2 + p0 : 2 * p0 + N) : 0;
+    const T* row = static_cast<const T*>(p.qkv) + i * p.row_stride;
+    const int H = p.Hq + 2 * p.Hkv;
+    const int hstep = p.warps_per_token * kHeads;
+    int h0 = part * kHeads + lane / LPH;
+    uint4 va[kUnroll], vb[kUnroll];
+    auto load = [&](int h) {
+#pragma unroll
+        for (int q = 0; q < kUnroll; ++q) {
+            va[q] = vb[q] = make_uint4(0u, 0u, 0u, 0u);
+            if (on && h + q * hstep < H) {
+                va[q] = __ldcs(reinterpret_cast<const uint4*>(row + static_cast<long long>(h + q * hstep) * D + e0));
+                vb[q] = __ldcs(reinterpret_cast<const uint4*>(row + static_cast<long long>(h + q * hstep) * D + e1));
+            }
+        }
+    };
+    // The first heads are on their way while the chain offsets -> sequence ->
+    // prefix -> page, angles is walked (rows behind the last token are in the
+    // array too; they are dropped below).
+    load(h0);
+    if (i >= p.off[p.nseq]) return;
     const int b = find_seq(p.off, p.nseq, i, lane);
     const int o = p.off[b], B = p.off[b + 1] - o, L = p.prefix_len[b], local = i - o;
     const long long slot = static_cast<long long>(L) + local;
@@ -115,12 +141,6 @@ __global__ void __launch_bounds__(kAppendThreads) qkv_append_kernel(const Append
         if (lane == 0) raise_error(p.err, DEVERR_INVALID);
         return;
     }
-    const int t = lane % LPH;
-    const bool on = kActive == LPH || t < kActive;
-    const int p0 = t * N;  // first of this lane's pairs
-    const bool rotated = on && p0 < p.rot / 2;
-    const bool split = rotated && !p.interleaved;
-    const int e0 = on ? (split ? p0 : 2 * p0) : 0, e1 = on ? (split ? p.rot / 2 + p0 : 2 * p0 + N) : 0;
     float cs[N], sn[N];
 #pragma unroll
     for (int j = 0; j < N; ++j) cs[j] = 1.0f, sn[j] = 0.0f;
@@ -134,24 +154,11 @@ __global__ void __launch_bounds__(kAppendThreads) qkv_append_kernel(const Append
             sn[j] = s.x, sn[j + 1] = s.y, sn[j + 2] = s.z, sn[j + 3] = s.w;
         }
     }
-    const T* row = static_cast<const T*>(p.qkv) + i * p.row_stride;
-    const int H = p.Hq + 2 * p.Hkv;
     const long long cache_row = (static_cast<long long>(page) * JT_PAGE_SIZE + slot % JT_PAGE_SIZE) * p.Hkv;
-    for (int h0 = part * kHeads + lane / LPH; __any_sync(0xFFFFFFFFu, h0 < H);
-         h0 += p.warps_per_token * kHeads * kUnroll) {
-        uint4 va[kUnroll], vb[kUnroll];
+    while (__any_sync(0xFFFFFFFFu, h0 < H)) {
 #pragma unroll
         for (int q = 0; q < kUnroll; ++q) {
-            const int h = h0 + q * p.warps_per_token * kHeads;
-            va[q] = vb[q] = make_uint4(0u, 0u, 0u, 0u);
-            if (on && h < H) {
-                va[q] = *reinterpret_cast<const uint4*>(row + static_cast<long long>(h) * D + e0);
-                vb[q] = *reinterpret_cast<const uint4*>(row + static_cast<long long>(h) * D + e1);
-            }
-        }
-#pragma unroll
-        for (int q = 0; q < kUnroll; ++q) {
-            const int h = h0 + q * p.warps_per_token * kHeads;
+            const int h = h0 + q * hstep;
             if (!__any_sync(0xFFFFFFFFu, h < H)) break;
             const bool is_q = h < p.Hq, is_v = h >= p.Hq + p.Hkv;
             const T* wt = static_cast<const T*>(is_q ? p.q_weight : p.k_weight);
@@ -203,6 +210,8 @@ __global__ void __launch_bounds__(kAppendThreads) qkv_append_kernel(const Append
             *reinterpret_cast<uint4*>(dst + e0) = va[q];
             *reinterpret_cast<uint4*>(dst + e1) = vb[q];
         }
+        h0 += hstep * kUnroll;
+        if (__any_sync(0xFFFFFFFFu, h0 < H)) load(h0);
     }
 }
 
