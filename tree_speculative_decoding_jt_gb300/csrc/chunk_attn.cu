@@ -257,40 +257,67 @@ __device__ __forceinline__ long long warp_sum(long long v) {
     return v;
 }
 
-// The planner (one warp): the total tile count, the range of work slot `work`
-// (of nwork) and the unit and tile that it starts at.  rec: also report the
-// sequences whose offsets or lengths are out of range.
+// Key tiles of one KV head with every unit's rounded up to a multiple of P.
+__device__ __forceinline__ int padded_head_tiles(const SeqInfo& s, int npt, int P) {
+    int t = 0;
+    for (int mp = 0; mp < s.np; ++mp) t += (unit_tiles(s, mp, npt) + P - 1) / P * P;
+    return t;
+}
+
+// The planner (one warp): the range of work slot `work` (of nwork) and the unit
+// and tile that it starts at.  Ranges are equal shares P of all tiles; with few
+// units (at most half the slots) every unit starts at a range's start instead, P
+// being large enough for the units' last ranges to be cut short: a slot then
+// has one piece, and no slot the ends of two units one after the other (one
+// token over 4096, 8 KV heads: 24 -> 20 us).  rec: also report the sequences
+// whose offsets or lengths are out of range.
 __device__ void plan_slot(const Params& p, Bars* bars, int lane, int work, int nwork, bool rec) {
-    long long total = 0;
+    SeqInfo mine;  // the sequence of this lane in the batch's last 32
+    mine.np = 0;
+    long long total = 0, units = 0;
     for (int base = 0; base < p.nseq; base += 32) {
         const int b = base + lane;
-        long long t = 0;
+        long long t = 0, u = 0;
         if (b < p.nseq) {
-            const SeqInfo s = load_seq(p, b);
-            if (s.np < 0) {
+            mine = load_seq(p, b);
+            if (mine.np < 0) {
                 if (rec) raise_error(p.err, DEVERR_INVALID);
             } else {
-                t = p.Hkv * head_tiles(s, p.npt);
+                t = p.Hkv * head_tiles(mine, p.npt);
+                u = static_cast<long long>(p.Hkv) * mine.np;
             }
+        } else {
+            mine.np = 0;
         }
         total += warp_sum(t);
+        units += warp_sum(u);
     }
     if (total > 0x7FFFFFFFll) {  // beyond the int tile arithmetic: refuse the launch's work
         if (rec && lane == 0) raise_error(p.err, DEVERR_INVALID);
         total = 0;
     }
     const int T_total = static_cast<int>(total);
-    const int P = T_total > 0 ? (T_total + nwork - 1) / nwork : 0;
+    int P = T_total > 0 ? (T_total + nwork - 1) / nwork : 0;
+    bool aligned = false;
+    if (T_total > 0 && 2 * units <= nwork) {
+        // sum of ceil(T_u / P) <= T_total / P + units <= nwork
+        const int share = nwork - static_cast<int>(units);
+        const int Pa = (T_total + share - 1) / share;
+        if (Pa <= P + 6) {  // the end of a piece costs a slot about six tiles' time
+            P = Pa;
+            aligned = true;
+        }
+    }
     const long long start = static_cast<long long>(work) * P;
-    int quota = (start < T_total) ? static_cast<int>(min(static_cast<long long>(P), T_total - start)) : 0;
     int found_b = -1, found_rel = 0;
     long long acc = 0;
-    for (int base = 0; base < p.nseq && quota > 0 && found_b < 0; base += 32) {
+    for (int base = 0; base < p.nseq && T_total > 0 && found_b < 0; base += 32) {
         const int b = base + lane;
         long long t = 0;
         if (b < p.nseq) {
-            const SeqInfo s = load_seq(p, b);
-            if (s.np > 0) t = p.Hkv * head_tiles(s, p.npt);
+            if (p.nseq > 32) mine = load_seq(p, b);
+            if (mine.np > 0)
+                t = p.Hkv * (aligned ? static_cast<long long>(padded_head_tiles(mine, p.npt, P)) : head_tiles(mine, p.npt));
         }
         long long incl = t;
 #pragma unroll
@@ -308,23 +335,45 @@ __device__ void plan_slot(const Params& p, Bars* bars, int lane, int work, int n
         }
         acc += __shfl_sync(0xFFFFFFFFu, incl, 31);
     }
-    if (found_b < 0) quota = 0;
-    int g = 0, mp = 0, t = 0;
-    if (quota > 0) {
-        const SeqInfo s = load_seq(p, found_b);
-        const int ht = static_cast<int>(head_tiles(s, p.npt));
-        g = found_rel / ht;
-        const int r = found_rel - g * ht;
-        int n = s.np;  // the last unit in [mp, mp + n) that starts at or before tile r
-        while (n > 1) {
-            const int step = (n + 31) / 32;
-            const bool le = lane * step < n && prefix_tiles(s, mp + lane * step, p.npt) <= r;
-            const unsigned m = __ballot_sync(0xFFFFFFFFu, le);
-            const int k = 31 - __clz(m | 1u);
-            mp += k * step;
-            n = min(step, n - k * step);
+    int quota = 0, g = 0, mp = 0, t = 0;
+    if (found_b >= 0) {
+        SeqInfo s;
+        if (p.nseq > 32) {
+            s = load_seq(p, found_b);
+        } else {
+            s.L = __shfl_sync(0xFFFFFFFFu, mine.L, found_b);
+            s.B = __shfl_sync(0xFFFFFFFFu, mine.B, found_b);
+            s.off = __shfl_sync(0xFFFFFFFFu, mine.off, found_b);
+            s.np = __shfl_sync(0xFFFFFFFFu, mine.np, found_b);
         }
-        t = r - static_cast<int>(prefix_tiles(s, mp, p.npt));
+        if (aligned) {
+            const int ht = padded_head_tiles(s, p.npt, P);
+            g = found_rel / ht;
+            t = found_rel - g * ht;
+            for (;; ++mp) {
+                const int T = unit_tiles(s, mp, p.npt), padded = (T + P - 1) / P * P;
+                if (t < padded) {
+                    quota = min(P, T - t);
+                    break;
+                }
+                t -= padded;
+            }
+        } else {
+            const int ht = static_cast<int>(head_tiles(s, p.npt));
+            g = found_rel / ht;
+            const int r = found_rel - g * ht;
+            int n = s.np;  // the last unit in [mp, mp + n) that starts at or before tile r
+            while (n > 1) {
+                const int step = (n + 31) / 32;
+                const bool le = lane * step < n && prefix_tiles(s, mp + lane * step, p.npt) <= r;
+                const unsigned m = __ballot_sync(0xFFFFFFFFu, le);
+                const int k = 31 - __clz(m | 1u);
+                mp += k * step;
+                n = min(step, n - k * step);
+            }
+            t = r - static_cast<int>(prefix_tiles(s, mp, p.npt));
+            quota = static_cast<int>(min(static_cast<long long>(P), T_total - start));
+        }
     }
     if (lane == 0) {
         bars->w_b = found_b;
@@ -1250,8 +1299,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (bars->merge_flag) {
                     if (cu.n <= 2)
                         merge_rows<D, 8, 2>(p, pc, cu, x, w4, lane);
-                    else
+                    else if (cu.n <= 8)
                         merge_rows<D, 2, 8>(p, pc, cu, x, w4, lane);
+                    else
+                        merge_rows<D, 1, 16>(p, pc, cu, x, w4, lane);
                 }
             }
         }

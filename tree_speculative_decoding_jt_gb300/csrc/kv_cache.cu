@@ -42,34 +42,75 @@ struct Append {
     float eps;
 };
 
-template <typename T>
-struct Vec;  // 16 bytes as floats
-template <>
-struct Vec<float> {
+// Two 16-byte vectors of a lane as N rotation pairs (a[j], b[j]) in fp32, and
+// back (rounded to the type): the halves of the vectors, or (kInter) neighbours.
+template <typename T, bool kInter>
+struct Pairs;
+template <bool kInter>
+struct Pairs<float, kInter> {
     static constexpr int N = 4;
-    static __device__ __forceinline__ void unpack(const uint4& u, float (&f)[4]) {
-        f[0] = __uint_as_float(u.x), f[1] = __uint_as_float(u.y), f[2] = __uint_as_float(u.z), f[3] = __uint_as_float(u.w);
-    }
-    static __device__ __forceinline__ uint4 pack(const float (&f)[4]) {
-        return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
-    }
-};
-template <>
-struct Vec<__nv_bfloat16> {
-    static constexpr int N = 8;
-    static __device__ __forceinline__ void unpack(const uint4& u, float (&f)[8]) {
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    static __device__ __forceinline__ void unpack(const uint4& u, const uint4& v, float (&a)[4], float (&b)[4]) {
+        const uint32_t w[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f[2 * i] = __uint_as_float(w[i] << 16);
-            f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        for (int j = 0; j < 4; ++j) {
+            a[j] = __uint_as_float(w[kInter ? 2 * j : j]);
+            b[j] = __uint_as_float(w[kInter ? 2 * j + 1 : 4 + j]);
         }
     }
-    static __device__ __forceinline__ uint4 pack(const float (&f)[8]) {
-        return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                          pack_bf16x2(f[6], f[7]));
+    static __device__ __forceinline__ void pack(const float (&a)[4], const float (&b)[4], uint4& u, uint4& v) {
+        uint32_t w[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            w[kInter ? 2 * j : j] = __float_as_uint(a[j]);
+            w[kInter ? 2 * j + 1 : 4 + j] = __float_as_uint(b[j]);
+        }
+        u = make_uint4(w[0], w[1], w[2], w[3]);
+        v = make_uint4(w[4], w[5], w[6], w[7]);
     }
 };
+template <bool kInter>
+struct Pairs<__nv_bfloat16, kInter> {
+    static constexpr int N = 8;
+    static __device__ __forceinline__ void unpack(const uint4& u, const uint4& v, float (&a)[8], float (&b)[8]) {
+        const uint32_t w[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float lo = __uint_as_float(w[j] << 16), hi = __uint_as_float(w[j] & 0xFFFF0000u);
+            if (kInter)
+                a[j] = lo, b[j] = hi;
+            else if (j < 4)
+                a[2 * j] = lo, a[2 * j + 1] = hi;
+            else
+                b[2 * j - 8] = lo, b[2 * j - 7] = hi;
+        }
+    }
+    static __device__ __forceinline__ void pack(const float (&a)[8], const float (&b)[8], uint4& u, uint4& v) {
+        uint32_t w[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            w[j] = kInter    ? pack_bf16x2(a[j], b[j])
+                   : j < 4 ? pack_bf16x2(a[(2 * j) & 7], a[(2 * j + 1) & 7])
+                           : pack_bf16x2(b[(2 * j) & 7], b[(2 * j + 1) & 7]);
+        u = make_uint4(w[0], w[1], w[2], w[3]);
+        v = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+};
+
+// Packed fp32 pair arithmetic: half the instructions of the scalar forms.
+__device__ __forceinline__ void mul2(float& d0, float& d1, float a0, float a1, float b0, float b1) {
+    asm("{\n\t.reg .b64 a, b, d;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d0), "=f"(d1)
+        : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+__device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1, float b0, float b1, float c0, float c1) {
+    asm("{\n\t.reg .b64 a, b, c, d;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d0), "=f"(d1)
+        : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c0), "f"(c1));
+}
 
 // The last sequence whose offset is at most i (one warp; a few steps of 32).
 __device__ __forceinline__ int find_seq(const int32_t* off, int nseq, int i, int lane) {
@@ -87,9 +128,10 @@ __device__ __forceinline__ int find_seq(const int32_t* off, int nseq, int i, int
 constexpr int kAppendThreads = 128;
 constexpr int kUnroll = 4;  // heads in flight per lane group
 
-template <typename T, int D, int LPH>
+template <typename T, int D, int LPH, bool kInter>
 __global__ void __launch_bounds__(kAppendThreads) qkv_append_kernel(const Append p) {
-    constexpr int N = Vec<T>::N;              // pairs per lane
+    using P = Pairs<T, kInter>;
+    constexpr int N = P::N;                   // pairs per lane
     constexpr int kActive = D / 2 / N;        // lanes of a head that hold elements
     constexpr int kHeads = 32 / LPH;          // heads per warp at a time
     pdl_wait();
@@ -102,7 +144,7 @@ __global__ void __launch_bounds__(kAppendThreads) qkv_append_kernel(const Append
     const bool on = kActive == LPH || t < kActive;
     const int p0 = t * N;  // first of this lane's pairs
     const bool rotated = on && p0 < p.rot / 2;
-    const bool split = rotated && !p.interleaved;
+    const bool split = rotated && !kInter;
     const int e0 = on ? (split ? p0 : 2 * p0) : 0, e1 = on ? (split ? p.rot / 2 + p0 : 2 * p0 + N) : 0;
     const T* row = static_cast<const T*>(p.qkv) + i * p.row_stride;
     const int H = p.Hq + 2 * p.Hkv;
@@ -141,19 +183,9 @@ __global__ void __launch_bounds__(kAppendThreads) qkv_append_kernel(const Append
         if (lane == 0) raise_error(p.err, DEVERR_INVALID);
         return;
     }
-    float cs[N], sn[N];
-#pragma unroll
-    for (int j = 0; j < N; ++j) cs[j] = 1.0f, sn[j] = 0.0f;
-    if (rotated) {
-        const float* tab = p.cos_sin + pos * p.rot + p0;
-#pragma unroll
-        for (int j = 0; j < N; j += 4) {
-            const float4 c = *reinterpret_cast<const float4*>(tab + j);
-            const float4 s = *reinterpret_cast<const float4*>(tab + p.rot / 2 + j);
-            cs[j] = c.x, cs[j + 1] = c.y, cs[j + 2] = c.z, cs[j + 3] = c.w;
-            sn[j] = s.x, sn[j + 1] = s.y, sn[j + 2] = s.z, sn[j + 3] = s.w;
-        }
-    }
+    int kind = 0;  // the heads that the matrices are for: 1 q, 2 k
+    float ca[N], sb[N], cb[N], sa[N];
+    const float* angles = p.cos_sin + pos * p.rot + p0;
     const long long cache_row = (static_cast<long long>(page) * JT_PAGE_SIZE + slot % JT_PAGE_SIZE) * p.Hkv;
     while (__any_sync(0xFFFFFFFFu, h0 < H)) {
 #pragma unroll
@@ -162,50 +194,68 @@ __global__ void __launch_bounds__(kAppendThreads) qkv_append_kernel(const Append
             if (!__any_sync(0xFFFFFFFFu, h < H)) break;
             const bool is_q = h < p.Hq, is_v = h >= p.Hq + p.Hkv;
             const T* wt = static_cast<const T*>(is_q ? p.q_weight : p.k_weight);
-            float fa[N], fb[N];
-            Vec<T>::unpack(va[q], fa);
-            Vec<T>::unpack(vb[q], fb);
+            // The norm's weight and the rotation as one matrix per pair: a' = a
+            // ca - b sb, b' = b cb + a sa, worked out once for the q and once
+            // for the k heads of the token.
+            if (on && !is_v && kind != (is_q ? 1 : 2)) {
+                kind = is_q ? 1 : 2;
+                float wa[N], wb[N];
+#pragma unroll
+                for (int j = 0; j < N; ++j) wa[j] = wb[j] = 1.0f;
+                if (wt) {
+                    const uint4 u = *reinterpret_cast<const uint4*>(wt + e0), v = *reinterpret_cast<const uint4*>(wt + e1);
+                    P::unpack(u, v, wa, wb);
+                }
+#pragma unroll
+                for (int j = 0; j < N; ++j) ca[j] = wa[j], cb[j] = wb[j], sa[j] = sb[j] = 0.0f;
+                if (rotated) {
+#pragma unroll
+                    for (int j = 0; j < N; j += 4) {
+                        const float4 c = *reinterpret_cast<const float4*>(angles + j);
+                        const float4 sn = *reinterpret_cast<const float4*>(angles + p.rot / 2 + j);
+                        const float cv[4] = {c.x, c.y, c.z, c.w}, sv[4] = {sn.x, sn.y, sn.z, sn.w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            ca[j + k] = wa[j + k] * cv[k];
+                            cb[j + k] = wb[j + k] * cv[k];
+                            sa[j + k] = wa[j + k] * sv[k];
+                            sb[j + k] = -wb[j + k] * sv[k];
+                        }
+                    }
+                }
+            }
             float ss = 0.0f;
+            float fa[N], fb[N];
+            P::unpack(va[q], vb[q], fa, fb);
+            if (wt) {
+                float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
-            for (int j = 0; j < N; ++j) ss = fmaf(fa[j], fa[j], fmaf(fb[j], fb[j], ss));
+                for (int j = 0; j < N; j += 2) {
+                    fma2(s0, s1, fa[j], fa[j + 1], fa[j], fa[j + 1], s0, s1);
+                    fma2(s0, s1, fb[j], fb[j + 1], fb[j], fb[j + 1], s0, s1);
+                }
+                ss = s0 + s1;
+            }
+            if (p.q_weight || p.k_weight)
 #pragma unroll
-            for (int d = LPH / 2; d >= 1; d >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, d);
+                for (int d = LPH / 2; d >= 1; d >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, d);
             if (!on || h >= H) continue;
             T* dst = is_q ? static_cast<T*>(p.q_out) + (static_cast<long long>(i) * p.Hq + h) * D
                           : static_cast<T*>(is_v ? p.v_cache : p.k_cache) +
                                 (cache_row + (is_v ? h - p.Hq - p.Hkv : h - p.Hq)) * D;
-            if (!is_v) {
-                if (wt) {
-                    const float inv = rsqrtf(ss * (1.0f / D) + p.eps);
-                    float wa[N], wb[N];
-                    Vec<T>::unpack(*reinterpret_cast<const uint4*>(wt + e0), wa);
-                    Vec<T>::unpack(*reinterpret_cast<const uint4*>(wt + e1), wb);
+            if (!is_v && (wt || rotated)) {
+                const float inv = wt ? rsqrtf(ss * (1.0f / D) + p.eps) : 1.0f;
 #pragma unroll
-                    for (int j = 0; j < N; ++j) fa[j] *= inv * wa[j], fb[j] *= inv * wb[j];
+                for (int j = 0; j < N; j += 2) {
+                    float x0, x1, y0, y1;
+                    mul2(x0, x1, fa[j], fa[j + 1], ca[j], ca[j + 1]);
+                    fma2(x0, x1, fb[j], fb[j + 1], sb[j], sb[j + 1], x0, x1);
+                    mul2(y0, y1, fb[j], fb[j + 1], cb[j], cb[j + 1]);
+                    fma2(y0, y1, fa[j], fa[j + 1], sa[j], sa[j + 1], y0, y1);
+                    mul2(fa[j], fa[j + 1], x0, x1, inv, inv);
+                    mul2(fb[j], fb[j + 1], y0, y1, inv, inv);
                 }
-                if (rotated) {
-                    if (split) {
-#pragma unroll
-                        for (int j = 0; j < N; ++j) {
-                            const float x = fa[j], y = fb[j];
-                            fa[j] = x * cs[j] - y * sn[j];
-                            fb[j] = y * cs[j] + x * sn[j];
-                        }
-                    } else {  // fa, fb: 2 N neighbouring elements
-#pragma unroll
-                        for (int j = 0; j < N / 2; ++j) {
-                            const float x = fa[2 * j], y = fa[2 * j + 1], z = fb[2 * j], w = fb[2 * j + 1];
-                            fa[2 * j] = x * cs[j] - y * sn[j];
-                            fa[2 * j + 1] = y * cs[j] + x * sn[j];
-                            fb[2 * j] = z * cs[N / 2 + j] - w * sn[N / 2 + j];
-                            fb[2 * j + 1] = w * cs[N / 2 + j] + z * sn[N / 2 + j];
-                        }
-                    }
-                }
-                if (wt || rotated) {
-                    va[q] = Vec<T>::pack(fa);
-                    vb[q] = Vec<T>::pack(fb);
-                }
+                P::pack(fa, fb, va[q], vb[q]);
             }
             *reinterpret_cast<uint4*>(dst + e0) = va[q];
             *reinterpret_cast<uint4*>(dst + e1) = vb[q];
@@ -217,19 +267,23 @@ __global__ void __launch_bounds__(kAppendThreads) qkv_append_kernel(const Append
 
 template <typename T, int D>
 static cudaError_t append_launch(Append prm, cudaStream_t st) {
-    constexpr int active = D / 2 / Vec<T>::N;
+    constexpr int active = D / 2 / Pairs<T, false>::N;
     constexpr int LPH = active <= 4 ? 4 : active <= 8 ? 8 : 16;
     static_assert(active <= 16, "head dim");
     const int H = prm.Hq + 2 * prm.Hkv, per = 32 / LPH;
-    // Few tokens: one head per lane group, so that a token's heads are read at
-    // once; many: four heads in flight per group, which amortises the token's
-    // offsets, page and angles.
-    const int fine = (H + per - 1) / per, coarse = (H + per * kUnroll - 1) / (per * kUnroll);
-    prm.warps_per_token = static_cast<long long>(prm.total) * fine <= 16ll * device_sm_count() ? fine : coarse;
+    // A token's heads go to as many warps as it takes to have about twelve warps
+    // per SM at work.  Many tokens get one warp each: the token's offsets, page
+    // and angles are looked up once, and its heads are read four per lane group
+    // at a time (22610 tokens of 32/8 heads, D 128: 98 us with one warp a token,
+    // 110 with two, 117 with three).  Few tokens get up to one lane group per
+    // head (761 tokens of 12/4 heads, D 96, fp32: 6.2 us with one, 4.7 with three).
+    const long long fine = (H + per - 1) / per;
+    prm.warps_per_token = static_cast<int>(
+        std::max(1ll, std::min(fine, (12ll * device_sm_count() + prm.total - 1) / prm.total)));
     const long long warps = static_cast<long long>(prm.total) * prm.warps_per_token;
     const long long blocks = (warps + kAppendThreads / 32 - 1) / (kAppendThreads / 32);
     if (blocks > 0x7FFFFFFFll) return cudaErrorInvalidValue;
-    return launch_kernel_pdl(qkv_append_kernel<T, D, LPH>, dim3(static_cast<unsigned>(blocks)), dim3(kAppendThreads), 0,
+    return launch_kernel_pdl(prm.interleaved ? qkv_append_kernel<T, D, LPH, true> : qkv_append_kernel<T, D, LPH, false>, dim3(static_cast<unsigned>(blocks)), dim3(kAppendThreads), 0,
                              st, prm);
 }
 
