@@ -475,10 +475,10 @@ jt_status jt_qkv_append(const void* qkv, int dtype, int64_t row_stride, const vo
  * Token i of sequence b, query head h (KV head h / (Hq/Hkv)) attends to slots
  * 0 .. L_b + i; what lies in other slots, infinities and NaN included, has no
  * effect on it.
- *   k_cache, v_cache, block_table, max_pages, num_pages, page_size, scale,
- *   dtype: as in jt_tree_attn_paged.  bf16: D in {64, 128}, Hq/Hkv <= 128;
+ *   k_cache, v_cache, block_table, max_pages, num_pages, page_size, dtype: as
+ *             in jt_tree_attn_paged.  bf16: D in {64, 128}, Hq/Hkv <= 128;
  *             fp32: D in {32, 64, 96, 128}, Hq/Hkv <= 64; else
- *             JT_ERR_UNSUPPORTED.
+ *             JT_ERR_UNSUPPORTED.  scale > 0.
  *   out:      [total_tokens, Hq, D] (dtype), lse: fp32 [total_tokens, Hq] or
  *             NULL, as in jt_tree_attn_paged.
  * The bf16 path runs on CTA pairs with the key tiles of all (sequence, KV

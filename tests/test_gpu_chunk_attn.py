@@ -302,3 +302,56 @@ def test_ragged_batches_in_a_row(dtype):
         for _ in range(6):
             out, lse = run(s, ws)
             assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_batches_of_mostly_idle_sequences(dtype):
+    """No new token at all; two of fifty sequences active."""
+    s = batch(24, [5, 0], [0, 0], 8, 2, 128, dtype, spare_rows=3)
+    s["new"] = [1, 1]  # max_chunk and workspace of a batch that could have had tokens
+    out = torch.full_like(s["q"], 5.0)
+    run(s, out=out)
+    assert bool((out == 5).all())
+    new = [0] * 50
+    new[17], new[41] = 3, 70
+    s = batch(25, [(7 * i) % 300 for i in range(50)], new, 8, 2, 128, dtype)
+    check(s, *run(s))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_shared_prefix_pages(dtype):
+    """Two sequences whose tables name the same physical pages for a common prefix."""
+    s = batch(26, [320, 320], [5, 40], 8, 2, 128, dtype)
+    s["table"][1, :20] = s["table"][0, :20]
+    check(s, *run(s))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_graphs_that_share_a_workspace_and_a_given_stream(dtype):
+    """Two captured graphs with one workspace, replayed in turn; calls on a
+    given stream that allocate their own workspace and outputs there."""
+    a, b = batch(27, [2000], [1], 32, 8, 128, dtype), batch(28, [100, 700, 5], [200, 1, 33], 16, 4, 128, dtype)
+    ws = workspace(a, b)
+    want = [tuple(t.clone() for t in run(s, ws)) for s in (a, b)]
+    graphs, outs = [], []
+    for s in (a, b):
+        out, lse = torch.empty_like(s["q"]), torch.empty(s["q"].shape[:2], device="cuda")
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            jt.jt_chunk_attn_paged(s["q"], s["k"], s["v"], s["table"], s["L"], s["off"], max_chunk=max(s["new"]), out=out,
+                                   lse=lse, ws=ws)
+        graphs.append(g)
+        outs.append((out, lse))
+    for _ in range(3):
+        for g, got, w in zip(graphs, outs, want):
+            got[0].zero_()
+            g.replay()
+            jt.jt_check(ws)
+            assert torch.equal(got[0], w[0]) and torch.equal(got[1], w[1])
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    got = [jt.jt_chunk_attn_paged(s["q"], s["k"], s["v"], s["table"], s["L"], s["off"], max_chunk=max(s["new"]), stream=st)
+           for s in (a, b, a, b)]
+    torch.cuda.current_stream().wait_stream(st)
+    for g, w in zip(got, want * 2):
+        assert torch.equal(g[0], w[0]) and torch.equal(g[1], w[1])

@@ -69,7 +69,7 @@ CHUNK = dict(q=A, k_cache=A, v_cache=A, dtype=1, block_table=A, max_pages=4, num
     (dict(block_table=None), INVALID), (dict(prefix_len=None), INVALID), (dict(chunk_off=None), INVALID),
     (dict(q=ODD), INVALID), (dict(out=ODD), INVALID), (dict(k_cache=ODD), INVALID), (dict(nseq=0), INVALID),
     (dict(nseq=65536), INVALID), (dict(total=-1), INVALID), (dict(max_chunk=0), INVALID), (dict(Hq=33), INVALID),
-    (dict(Hkv=0), INVALID), (dict(page_size=8), INVALID), (dict(scale=float("inf")), INVALID), (dict(dtype=3), INVALID),
+    (dict(Hkv=0), INVALID), (dict(page_size=8), INVALID), (dict(scale=float("inf")), INVALID), (dict(scale=0.0), INVALID), (dict(scale=-0.1), INVALID), (dict(dtype=3), INVALID),
     (dict(max_pages=0), INVALID), (dict(num_pages=0), INVALID), (dict(D=96), UNSUPPORTED), (dict(D=256), UNSUPPORTED),
     (dict(dtype=0, D=80), UNSUPPORTED), (dict(Hq=129, Hkv=1), UNSUPPORTED), (dict(dtype=0, Hq=65, Hkv=1), UNSUPPORTED),
     (dict(dtype=0, nseq=65535, Hq=64, Hkv=64, max_chunk=1 << 30), UNSUPPORTED),

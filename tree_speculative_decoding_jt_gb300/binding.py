@@ -598,18 +598,26 @@ def _workspace_of(ws, idx):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # no Stream object made
 
 
-def _packed(op, idx, stream, *args):
-    """jt_call on the tensors' device and its current stream (or the given one)."""
+def _packed(op, idx, *args):
+    """jt_call on the tensors' device and its current stream."""
     lib = load()
     s = _PACK[op]
     if idx != torch.cuda.current_device():
         with torch.cuda.device(idx):
-            return lib.jt_call(op, s.pack(*args, _stream(stream)), s.size)
-    if stream is None and _raw_stream is not None:
-        raw = _raw_stream(idx)
-    else:
-        raw = _stream(stream)
-    return lib.jt_call(op, s.pack(*args, raw), s.size)
+            return lib.jt_call(op, s.pack(*args, _stream()), s.size)
+    return lib.jt_call(op, s.pack(*args, _raw_stream(idx) if _raw_stream is not None else _stream()), s.size)
+
+
+def _on_given_stream(fn):
+    """Make a given stream the current one for the call, so that what the call
+    allocates (and frees, and zeroes) belongs to the stream that uses it."""
+    @functools.wraps(fn)
+    def wrapper(*args, stream=None, **kwargs):
+        if stream is None:
+            return fn(*args, **kwargs)
+        with torch.cuda.stream(stream):
+            return fn(*args, **kwargs)
+    return wrapper
 
 
 def rope_table(max_pos, rot_dim, theta=1e6, device=None):
@@ -621,8 +629,9 @@ def rope_table(max_pos, rot_dim, theta=1e6, device=None):
     return torch.cat([a.cos(), a.sin()], 1).float().to(device or "cuda")
 
 
+@_on_given_stream
 def jt_qkv_append(qkv, Hq, k_cache, v_cache, block_table, prefix_len, tree_off, q_weight=None, k_weight=None,
-                  eps=1e-6, cos_sin=None, interleaved=False, depth=None, q_out=None, ws=None, stream=None):
+                  eps=1e-6, cos_sin=None, interleaved=False, depth=None, q_out=None, ws=None):
     """Per-head norm of q and k, position rotation, and the write of k and v
     into the paged cache, from the packed projection.
 
@@ -630,7 +639,8 @@ def jt_qkv_append(qkv, Hq, k_cache, v_cache, block_table, prefix_len, tree_off, 
     Hkv, D]; q_weight, k_weight [D] or None; cos_sin fp32 [max_pos, rot_dim] or
     None (see rope_table); depth int32 [total] (tree nodes: position L_b +
     depth) or None (position L_b + i).  Returns q_out [total, Hq, D] (None for
-    Hq = 0); the caches are updated in place."""
+    Hq = 0); the caches are updated in place.  stream (keyword): the stream to
+    run on, as in every call here; default the current one."""
     idx, dtype = _lead(qkv, "qkv")
     kind, kv_shape = qkv.dtype, k_cache.shape
     if len(kv_shape) != 4:
@@ -672,7 +682,7 @@ def jt_qkv_append(qkv, Hq, k_cache, v_cache, block_table, prefix_len, tree_off, 
         q_ptr = q_out.data_ptr()
     if ws is None:
         ws = workspace(256, qkv.device)
-    rc = _packed(JT_OP_QKV_APPEND, idx, stream, qkv.data_ptr(), dtype, row, qw, kw, eps, table, max_pos, rot,
+    rc = _packed(JT_OP_QKV_APPEND, idx, qkv.data_ptr(), dtype, row, qw, kw, eps, table, max_pos, rot,
                  1 if interleaved else 0, steps, block_table.data_ptr(), max_pages, num_pages, prefix_len.data_ptr(),
                  tree_off.data_ptr(), nseq, total, Hq, Hkv, D, page, q_ptr, k_cache.data_ptr(), v_cache.data_ptr(),
                  ws.data_ptr(), _workspace_of(ws, idx))
@@ -681,8 +691,9 @@ def jt_qkv_append(qkv, Hq, k_cache, v_cache, block_table, prefix_len, tree_off, 
     return q_out
 
 
+@_on_given_stream
 def jt_chunk_attn_paged(q, k_cache, v_cache, block_table, prefix_len, chunk_off, scale=None, max_chunk=None,
-                        out=None, lse=None, ws=None, stream=None, with_lse=True):
+                        out=None, lse=None, ws=None, with_lse=True):
     """Causal attention of new tokens (chunks of any length, ragged) over a
     paged KV cache that already holds their keys and values.
 
@@ -719,7 +730,7 @@ def jt_chunk_attn_paged(q, k_cache, v_cache, block_table, prefix_len, chunk_off,
         with torch.cuda.device(idx):  # sized for the tensors' device
             ws = workspace(jt_workspace_size(JT_OP_CHUNK_ATTN, nseq, 0, 0, 0, total, Hq, Hkv, D, max_pages, max_chunk),
                            q.device)
-    rc = _packed(JT_OP_CHUNK_ATTN, idx, stream, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), dtype,
+    rc = _packed(JT_OP_CHUNK_ATTN, idx, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), dtype,
                  block_table.data_ptr(), max_pages, num_pages, prefix_len.data_ptr(), chunk_off.data_ptr(), nseq,
                  total, max_chunk, Hq, Hkv, D, page, scale, out.data_ptr(), 0 if lse is None else lse.data_ptr(),
                  ws.data_ptr(), _workspace_of(ws, idx))
@@ -728,8 +739,8 @@ def jt_chunk_attn_paged(q, k_cache, v_cache, block_table, prefix_len, chunk_off,
     return out, lse
 
 
-def jt_kv_commit(k_cache, v_cache, block_table, prefix_len, tree_off, accept_len, path, new_prefix=None, ws=None,
-                 stream=None):
+@_on_given_stream
+def jt_kv_commit(k_cache, v_cache, block_table, prefix_len, tree_off, accept_len, path, new_prefix=None, ws=None):
     """Move the accepted path's keys and values behind the prefix and advance
     the prefix lengths.
 
@@ -757,7 +768,7 @@ def jt_kv_commit(k_cache, v_cache, block_table, prefix_len, tree_off, accept_len
         _like(new_prefix, "new_prefix", torch.int32, idx, (nseq,))
     if ws is None:
         ws = workspace(jt_workspace_size(JT_OP_KV_COMMIT, nseq), k_cache.device)
-    rc = _packed(JT_OP_KV_COMMIT, idx, stream, k_cache.data_ptr(), v_cache.data_ptr(), dtype, layers,
+    rc = _packed(JT_OP_KV_COMMIT, idx, k_cache.data_ptr(), v_cache.data_ptr(), dtype, layers,
                  num_pages * page * Hkv * D, block_table.data_ptr(), max_pages, num_pages, prefix_len.data_ptr(),
                  tree_off.data_ptr(), accept_len.data_ptr(), path.data_ptr(), nseq, width - 1, Hkv, D, page,
                  new_prefix.data_ptr(), ws.data_ptr(), _workspace_of(ws, idx))

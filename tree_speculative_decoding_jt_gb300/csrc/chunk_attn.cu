@@ -6,9 +6,8 @@
 // the slots 0 .. L_b + i:
 //     out = sum_s exp(scale q.k_s - m) v_s / l,  l = sum_s exp(scale q.k_s - m),
 // one pass over the keys with the running maximum m and sum l (fp32), P =
-// exp(...) rounded to bf16 for the second product (relative 2^-9 each, the
-// rounding of the inputs themselves; l sums the unrounded values), the output
-// rounded once.
+// exp(...) rounded to bf16 for the second product (at most 2^-8 relative, as the
+// inputs are; l sums the unrounded values), the output rounded once.
 //
 // Work.  A unit is (sequence b, KV head g, query-tile pair mp): two 128-row
 // query tiles of npt = 128 / G new tokens x the G query heads of KV head g
@@ -24,7 +23,7 @@
 // number of tiles.  A unit cut by a range boundary leaves fp32 partials; the
 // slot that finishes its last piece merges them, summing in piece order.
 //
-// Warps per CTA (512 threads; warp 15 idles):
+// Warps per CTA (512 threads):
 //   0-3 / 4-7  softmax of the tiles with even / odd number, one query row per
 //              thread.  Warps w and w + 4 hold the same 32 rows, and each warp
 //              has two tiles' time for one tile's softmax.  P of all tiles of a
@@ -39,10 +38,13 @@
 //   8-11       epilogue: O of a piece to the output or to its partial, and the
 //              merges, while the softmax warps are at the next piece's tiles;
 //   12 / 14    TMA producers of Q and K / of V, one box per 16-token page;
-//   13         TMEM allocation; in the pair's leader, the MMA issuer.
+//   13 / 15    in the pair's leader, the MMA issuers of O += P V and of S = Q K^T:
+//              one warp for both spends longer on its waits, issues and commits
+//              than the MMAs take (1163 us where two take 1123: 8192 tokens on
+//              8192, 32/8 heads, D 128); 13 also allocates TMEM.
 // TMEM (512 columns): S0, S1, S2 (P of a tile overwrites the first half of its
-// S) and O.  The MMA warp issues QK up to three tiles ahead, across units; Q is
-// double buffered.
+// S) and O.  S runs up to three tiles ahead of O, across units; Q is double
+// buffered.
 #include <algorithm>
 
 #include "jt_common.cuh"
@@ -115,7 +117,7 @@ struct Bars {
     uint64_t p_full[3];             // leader: P of the tile in the S buffer, from 8 softmax warps
     uint64_t o_done[3];             // one phase per PV of a tile t with t mod 3 == index
     uint64_t o_free;                // leader: the pair's 8 epilogue warps have read the piece's O
-    uint64_t mma_final;             // every MMA of the pair has completed
+    uint64_t mma_final;             // every MMA of the pair has completed (both issuers)
     uint64_t x_bar[kRing][4];       // warps w, w + 4 have left a piece's maxima and sums for the epilogue
     uint64_t msync;                 // this CTA's 4 epilogue warps meet (merge of a cut unit)
     uint32_t tmem_base;
@@ -441,60 +443,84 @@ __device__ __forceinline__ void fadd2(float& d0, float& d1, float a0, float a1, 
         : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
 }
 
-// The loops over the four 32-column chunks of a score row stay loops: unrolled
-// over the whole row, the softmax's code pushed the MMA warp's out of the
-// instruction caches, and the MMA warp's loop then took longer than its MMAs
-// (2000 cycles a tile where the MMAs need 1080).
+// The softmax's code is kept small (loops over a row's chunks, masks out of
+// line): unrolled over the whole row with the masks in place, it pushed itself and
+// the MMA warp's loop out of the instruction caches, and a tile took 2000 cycles
+// where its MMAs need 1080.  A chunk of 32 columns loads while the one before is
+// worked on.
 
-// Columns at or past `visible` -> -inf.
-__device__ __forceinline__ void mask_chunk(uint32_t (&c)[32], int visible) {
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-        if (i >= visible) c[i] = __float_as_uint(-INFINITY);
-}
-
-// Maximum of the visible scores of this thread's row.
-__device__ __forceinline__ float row_max(uint32_t tS, bool diag, int visible) {
-    float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+// Scores at or past column `visible` of this thread's row -> -inf, in tensor
+// memory (a unit's last tiles only).
+__device__ __noinline__ void mask_row(uint32_t tS, int visible) {
 #pragma unroll 1
     for (int q = 0; q < 4; ++q) {
         uint32_t c[32];
         tmem_ld32(tS + 32 * q, c);
         tmem_wait_ld();
-        if (diag) mask_chunk(c, visible - 32 * q);
 #pragma unroll
-        for (int i = 0; i < 32; i += 2)
-            m[(i >> 1) & 3] = fmax3(m[(i >> 1) & 3], __uint_as_float(c[i]), __uint_as_float(c[i + 1]));
+        for (int i = 0; i < 32; ++i)
+            if (32 * q + i >= visible) c[i] = __float_as_uint(-INFINITY);
+        tmem_st32(tS + 32 * q, c);
+    }
+    tmem_wait_st();
+}
+
+__device__ __forceinline__ void max_chunk(const uint32_t (&c)[32], float (&m)[4]) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 2)
+        m[(i >> 1) & 3] = fmax3(m[(i >> 1) & 3], __uint_as_float(c[i]), __uint_as_float(c[i + 1]));
+}
+
+// Maximum of this thread's score row.
+__device__ __forceinline__ float row_max(uint32_t tS) {
+    float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+    uint32_t c[32], d[32];
+    tmem_ld32(tS, c);
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+        tmem_wait_ld();
+        tmem_ld32(tS + 64 * h + 32, d);
+        max_chunk(c, m);
+        tmem_wait_ld();
+        if (h == 0) tmem_ld32(tS + 64, c);
+        max_chunk(d, m);
     }
     return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+
+// One chunk's exponentials: packed to bf16 pairs into 16 columns at tP, summed.
+__device__ __forceinline__ void exp_chunk(const uint32_t (&c)[32], uint32_t tP, float sl2, float m, float (&a)[4]) {
+    uint32_t pk[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        float x0, x1;
+        ffma2(x0, x1, __uint_as_float(c[2 * i]), __uint_as_float(c[2 * i + 1]), sl2, sl2, -m, -m);
+        const float e0 = ex2_approx(x0);
+        const float e1 = ex2_approx(x1);
+        const int k = 2 * (i & 1);
+        fadd2(a[k], a[k + 1], a[k], a[k + 1], e0, e1);
+        pk[i] = pack_bf16x2(e0, e1);
+    }
+    tmem_st16(tP, pk);
 }
 
 // P = exp2(s * sl2 - m), packed to bf16 pairs into the first 64 columns of the
 // S region (chunk q writes columns 16 q .. 16 q + 15, which chunks up to q have
 // been read from); returns the sum of the unrounded values.
-__device__ __forceinline__ float row_exp(uint32_t tS, bool diag, int visible, float sl2, float m) {
-    float a0 = 0.0f, a1 = 0.0f, b0 = 0.0f, b1 = 0.0f;
+__device__ __forceinline__ float row_exp(uint32_t tS, float sl2, float m) {
+    float a[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    uint32_t c[32], d[32];
+    tmem_ld32(tS, c);
 #pragma unroll 1
-    for (int q = 0; q < 4; ++q) {
-        uint32_t c[32], pk[16];
-        tmem_ld32(tS + 32 * q, c);
+    for (int h = 0; h < 2; ++h) {
         tmem_wait_ld();
-        if (diag) mask_chunk(c, visible - 32 * q);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            float x0, x1;
-            ffma2(x0, x1, __uint_as_float(c[2 * i]), __uint_as_float(c[2 * i + 1]), sl2, sl2, -m, -m);
-            const float e0 = ex2_approx(x0);
-            const float e1 = ex2_approx(x1);
-            if (i & 1)
-                fadd2(b0, b1, b0, b1, e0, e1);
-            else
-                fadd2(a0, a1, a0, a1, e0, e1);
-            pk[i] = pack_bf16x2(e0, e1);
-        }
-        tmem_st16(tS + 16 * q, pk);
+        tmem_ld32(tS + 64 * h + 32, d);
+        exp_chunk(c, tS + 32 * h, sl2, m, a);
+        tmem_wait_ld();
+        if (h == 0) tmem_ld32(tS + 64, c);
+        exp_chunk(d, tS + 32 * h + 16, sl2, m, a);
     }
-    return (a0 + a1) + (b0 + b1);
+    return (a[0] + a[1]) + (a[2] + a[3]);
 }
 
 // The partner warp's word for tile t, (t + 1, m) (bounded: false when it gives
@@ -618,6 +644,30 @@ __device__ __noinline__ void redo_row(const Params& p, int b, int L, int g, int 
 // Operand descriptors are stepped by adding the byte offset / 16 to the
 // start-address field.  The whole MMA warp calls these; one elected lane issues.
 
+// The pair's MMAs with the low words of their operands' descriptors in 32 bits
+// (the start address steps; the high words are constants), which halves the
+// address arithmetic between two MMAs.
+__device__ __forceinline__ void mma_ss32(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc,
+                                         uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts32(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t hi, uint32_t idesc,
+                                         uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+        "mov.b64 b, {%2, %3};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
 // S = Q K^T over the pair: D / 16 MMAs of M = 256, N = 128, K = 16; then the
 // commits that report S, the K stage and, past a piece's last tile, its Q.
 template <int D>
@@ -630,7 +680,8 @@ __device__ __forceinline__ void issue_qk(uint32_t tS, uint64_t dq, uint64_t dk, 
         for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t qo = ((kk >> 2) * SL::kQChunk + (kk & 3) * 32) >> 4;
             const uint32_t ko = ((kk >> 2) * SL::kKChunk + (kk & 3) * 32) >> 4;
-            mma_ss_pair(tS, dq + qo, dk + ko, idesc, kk > 0 ? 1u : 0u);
+            mma_ss32(tS, static_cast<uint32_t>(dq) + qo, static_cast<uint32_t>(dk) + ko, (1024u >> 4) | 1u << 14 | 2u << 29,
+                     idesc, kk > 0 ? 1u : 0u);
         }
         mma_commit_pair(s_full);
         mma_commit_pair(k_empty);
@@ -649,7 +700,8 @@ __device__ __forceinline__ void issue_pv(uint32_t tO, uint32_t tP, uint64_t dv, 
     if (elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < kTileN / 16; ++kk)
-            mma_ts_pair(tO, tP + kk * 8, dv + kk * ((16 * Smem<D>::kVRow) >> 4), idesc, (accumulate || kk > 0) ? 1u : 0u);
+            mma_ts32(tO, tP + kk * 8, static_cast<uint32_t>(dv) + kk * ((16 * Smem<D>::kVRow) >> 4),
+                     static_cast<uint32_t>(dv >> 32), idesc, (accumulate || kk > 0) ? 1u : 0u);
         mma_commit_pair(o_done);
         mma_commit_pair(v_empty);
     }
@@ -814,7 +866,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             mbar_init(&bars->o_done[x], 1);
         }
         mbar_init(&bars->o_free, 8);
-        mbar_init(&bars->mma_final, 1);
+        mbar_init(&bars->mma_final, 2);
         for (int i = 0; i < kRing; ++i)
             for (int w = 0; w < 4; ++w) mbar_init(&bars->x_bar[i][w], 2);
         mbar_init(&bars->msync, 4);
@@ -968,73 +1020,62 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     for (int j = max(0, jj - VS); j < jj; ++j)
                         mbar_wait(&bars->v_full[j % VS], (j / VS) & 1, p.err, nullptr);
             }
-        } else if (rank == 0 && warp == 13) {
-            // -------------------------------------------------------- MMA
-            // One thread issues both products, in an order that the tensor
-            // pipe then keeps: QK(t + 3) right behind PV(t), which frees its S
-            // buffer.  (Two issuing warps, with QK waiting for PV's completion,
-            // took 1416 us where this takes 1315: 8192 tokens on 8192.)
+        } else if (rank == 0 && warp == 15) {
+            // ------------------------------------------------ MMA: S = Q K^T
             const uint64_t dq0 = smem_desc_sw128(smem_u32(sQ), 16, 1024);
             const uint64_t dk0 = smem_desc_sw128(smem_u32(sK), 16, 1024);
-            const uint64_t dv0 = v_desc<D>(smem_u32(sV));
-            Walker w;  // of the QKs, which run up to three tiles ahead of the PVs, across pieces
+            Walker w;
             w.init(p, bars, work);
-            int issued = 0, left_q = 0;     // QKs issued; tiles left of their piece
-            int kst = 0, qb = 0, qs = 1;    // K stage, S buffer and Q slot of the next QK
-            uint32_t kpar = 0, qpar = 1;    // phase parities of K stage and Q slot
-            uint32_t ends = 0;              // bit i: tile jj + i is the last of its piece
-            bool q_here = false;            // the piece's Q has landed
-            int jj = 0, st = 0, b = 0;      // PVs issued; V stage and S buffer of the next one
-            uint32_t vpar = 0, ppar = 0, opar = 1;
-            bool first = true;              // the next PV is the first of its piece
+            Piece pc;
+            int qs = 0, st = 0, b = 0;              // Q slot, K stage and S buffer of the tile
+            uint32_t qpar = 0, kpar = 0, opar = 1;  // their phase parities (S buffer: PV of its last tile)
+            int fresh = 3;                          // S buffers that no tile has used
             bool ok = true;
-            for (;;) {
-                // S(t mod 3) is free for QK(t + 3) once PV(t) is issued.  QK(jj)
-                // must be on its way before P(jj) is awaited; later QKs go now
-                // only if their operands have landed, so that a late K never
-                // holds back the next PV.
-                while (issued < min(jj + 3, quota)) {
-                    if (left_q == 0) {
-                        Piece pq;
-                        w.next(p, pq);
-                        left_q = pq.nt;
-                        qs ^= 1;
-                        if (qs == 0) qpar ^= 1;
-                        q_here = false;
-                    }
-                    if (issued <= jj) {
-                        ok = (q_here || mbar_wait_warp(&bars->q_full[qs], qpar, p.err, abort)) &&
-                             mbar_wait_warp(&bars->k_full[kst], kpar, p.err, abort);
-                        if (!ok) break;
-                    } else if (!(q_here || __all_sync(0xFFFFFFFFu, mbar_try_wait(&bars->q_full[qs], qpar))) ||
-                               !__all_sync(0xFFFFFFFFu, mbar_try_wait(&bars->k_full[kst], kpar))) {
-                        break;
-                    }
-                    q_here = true;
-                    --left_q;
+            while (ok && w.next(p, pc)) {
+                ok = mbar_wait_warp(&bars->q_full[qs], qpar, p.err, abort);
+                const uint64_t dq = dq0 + qs * (SL::kQBytes >> 4);
+                for (int left = pc.nt; ok && left > 0; --left) {
+                    ok = mbar_wait_warp(&bars->k_full[st], kpar, p.err, abort);
+                    // S(t mod 3) is free once PV(t - 3) has read the P in it
+                    if (fresh > 0)
+                        --fresh;
+                    else
+                        ok = ok && mbar_wait_warp(&bars->o_done[b], opar, p.err, abort);
+                    if (!ok) break;
                     tc_fence_after();
-                    issue_qk<D>(tmem + 128 * qb, dq0 + qs * (SL::kQBytes >> 4), dk0 + kst * (SL::kKHalf >> 4),
-                                &bars->s_full[qb], &bars->k_empty[kst], left_q == 0 ? &bars->q_empty[qs] : nullptr);
-                    if (left_q == 0) ends |= 1u << (issued - jj);
-                    ++issued;
-                    if (++kst == KS) kst = 0, kpar ^= 1;
-                    if (++qb == 3) qb = 0;
+                    issue_qk<D>(tmem + 128 * b, dq, dk0 + st * (SL::kKHalf >> 4), &bars->s_full[b], &bars->k_empty[st],
+                                left == 1 ? &bars->q_empty[qs] : nullptr);
+                    if (++st == KS) st = 0, kpar ^= 1;
+                    if (++b == 3) b = 0, opar ^= 1;
                 }
-                if (!ok || jj == quota) break;
-                ok = mbar_wait_warp(&bars->v_full[st], vpar, p.err, abort);
+                qs ^= 1;
+                if (qs == 0) qpar ^= 1;
+            }
+            commit_warp(&bars->mma_final);
+        } else if (rank == 0 && warp == 13) {
+            // ------------------------------------------------ MMA: O += P V
+            const uint64_t dv0 = v_desc<D>(smem_u32(sV));
+            Walker w;
+            w.init(p, bars, work);
+            Piece pc;
+            int st = 0, b = 0;                      // V stage and S buffer of the tile
+            uint32_t vpar = 0, ppar = 0, fpar = 1;
+            bool ok = true, first = true;
+            while (ok && w.next(p, pc)) {
                 // the previous piece's O has been read out
-                if (ok && first && jj > 0) ok = mbar_wait_warp(&bars->o_free, opar, p.err, abort);
-                ok = ok && mbar_wait_warp(&bars->p_full[b], ppar, p.err, abort);
-                if (!ok) break;
-                tc_fence_after();
-                issue_pv<D>(tmem + 384, tmem + 128 * b, dv0 + st * (SL::kVHalf >> 4), !first, &bars->o_done[b],
-                            &bars->v_empty[st]);
-                first = ends & 1u;
-                if (first) opar ^= 1;
-                ends >>= 1;
-                ++jj;
-                if (++st == VS) st = 0, vpar ^= 1;
-                if (++b == 3) b = 0, ppar ^= 1;
+                if (!first) ok = mbar_wait_warp(&bars->o_free, fpar, p.err, abort);
+                first = false;
+                fpar ^= 1;
+                for (int j = 0; ok && j < pc.nt; ++j) {
+                    ok = mbar_wait_warp(&bars->v_full[st], vpar, p.err, abort) &&
+                         mbar_wait_warp(&bars->p_full[b], ppar, p.err, abort);
+                    if (!ok) break;
+                    tc_fence_after();
+                    issue_pv<D>(tmem + 384, tmem + 128 * b, dv0 + st * (SL::kVHalf >> 4), j > 0, &bars->o_done[b],
+                                &bars->v_empty[st]);
+                    if (++st == VS) st = 0, vpar ^= 1;
+                    if (++b == 3) b = 0, ppar ^= 1;
+                }
             }
             commit_warp(&bars->mma_final);
         }
@@ -1091,9 +1132,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 float m_o = -INFINITY;  // the partner's m after the tile before: what O is scaled by
                 if (warp_on) {
                     const uint32_t tS = tmem + 128 * b + lane_off;
-                    const bool diag = j >= jdiag;
-                    const int visible = visible0 - j * kTileN;
-                    const float mx_s = row_max(tS, diag, visible) * sl2;
+                    if (j >= jdiag) mask_row(tS, visible0 - j * kTileN);
+                    const float mx_s = row_max(tS) * sl2;
                     const float m_before = m_run;
                     if (j < 2 && t > 0) {
                         // j = 1: the row's first maximum; j = 0: the word to be
@@ -1107,7 +1147,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     if (mx_s > m_run + kRescaleLog2 || m_run == -INFINITY) m_run = fmaxf(m_run, mx_s);
                     if (j == 0) tell_partner(t, m_run);  // early: the partner's first tile waits for it
                     // P = exp2(s*scale*log2e - m), written over S (bf16 pairs)
-                    float sum = row_exp(tS, diag, visible, sl2, m_run == -INFINITY ? 0.0f : m_run);
+                    float sum = row_exp(tS, sl2, m_run == -INFINITY ? 0.0f : m_run);
                     if (j > 0) {
                         if (j > 1 && !partner_max(word_of(t - 1), t - 1, m_o, p.err, abort)) {
                             ok = false;

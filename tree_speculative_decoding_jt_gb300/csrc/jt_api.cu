@@ -365,7 +365,7 @@ jt_status jt_chunk_attn_paged(const void* q, const void* k_cache, const void* v_
                               size_t ws_bytes, jt_stream_t stream) {
     JT_RANGE("jt_chunk_attn_paged");
     if (total_tokens < 0 || nseq < 1 || nseq > 65535 || max_chunk < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 ||
-        D < 1 || max_pages < 1 || num_pages < 1 || page_size != JT_PAGE_SIZE || !isfinite(scale) ||
+        D < 1 || max_pages < 1 || num_pages < 1 || page_size != JT_PAGE_SIZE || !isfinite(scale) || !(scale > 0.0f) ||
         (dtype != JT_DTYPE_BF16 && dtype != JT_DTYPE_F32))
         return JT_ERR_INVALID;
     const bool bf16 = dtype == JT_DTYPE_BF16;
