@@ -13,7 +13,7 @@ from kv_util import HALF_STEP, PAGE, chunk_bounds, chunk_ref, slots
 from test_gpu_kv_cache import bits, heads_ref
 
 pytestmark = pytest.mark.gpu
-Hq, Hkv, D, V, LAYERS = 16, 4, 128, 400, 2
+Hq, Hkv, D, V, LAYERS = 8, 4, 128, 400, 2
 I32 = dict(dtype=torch.int32, device="cuda")
 
 

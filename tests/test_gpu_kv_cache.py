@@ -101,7 +101,7 @@ APPEND = [
     ([0], [1], 32, 8, 128, BF16, 128, {}),
     ([100, 5, 0, 31], [40, 0, 17, 1], 32, 8, 128, BF16, 128, {}),
     ([100, 5, 0, 31], [40, 0, 17, 1], 32, 8, 128, BF16, 128, dict(tree=True)),
-    ([7, 300], [600, 900], 16, 4, 128, BF16, 64, dict(interleaved=True)),
+    ([7, 300], [600, 900], 12, 4, 128, BF16, 64, dict(interleaved=True)),
     ([7, 300], [3, 9], 6, 2, 64, BF16, 32, dict(norm=False)),
     ([7, 300], [3, 9], 5, 1, 64, BF16, 64, dict(interleaved=True, stride=64)),
     ([20, 1], [33, 2], 0, 3, 128, BF16, 128, {}),                       # keys and values only

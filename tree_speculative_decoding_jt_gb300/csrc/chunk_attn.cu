@@ -56,7 +56,13 @@ namespace chunk {
 constexpr int kThreads = 512;
 // Registers: 128 a thread at launch; the softmax and epilogue warps take what
 // the others give up: 256 * 136 + 128 * 160 + 128 * 80 = 512 * 128.
+constexpr int kLaunchRegs = 65536 / kThreads;
 constexpr int kSoftmaxRegs = 136, kEpilogueRegs = 160, kOtherRegs = 80;
+// setmaxnreg.inc may not go below the launch's count, .dec not above it, and
+// what the warps take must not exceed what the block was launched with.
+static_assert(kSoftmaxRegs >= kLaunchRegs && kEpilogueRegs >= kLaunchRegs && kOtherRegs <= kLaunchRegs);
+static_assert(kSoftmaxRegs % 8 == 0 && kEpilogueRegs % 8 == 0 && kOtherRegs % 8 == 0);
+static_assert(256 * kSoftmaxRegs + 128 * kEpilogueRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs);
 constexpr int kRing = 4;     // pieces whose rows' sums may wait for the epilogue
 constexpr int kTileN = 128;  // keys per KV tile
 constexpr int kTileM = 128;  // query rows per query tile
