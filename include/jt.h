@@ -448,8 +448,10 @@ jt_status jt_verify_accept_stochastic(const float* target_logits, const float* d
  * the bits are copied.  A token whose sequence has contents out of range,
  * whose page is outside the pool or whose position is not below max_pos is
  * skipped (nothing of it is written) and raises JT_ERR_INVALID (device-side).
- * total_nodes = 0 does nothing.  qkv, weights, cos_sin, q_out and the caches
- * are 16-byte aligned (row_stride included) and do not overlap.
+ * total_nodes = 0 does nothing; rows at or beyond tree_off[nseq] are ignored.
+ * qkv, weights, cos_sin, q_out and the caches are 16-byte aligned (row_stride
+ * included); qkv, q_out, k_cache and v_cache do not overlap (JT_ERR_INVALID).  A
+ * slot belongs to one token of the call.
  * Workspace: 256 bytes.
  */
 jt_status jt_qkv_append(const void* qkv, int dtype, int64_t row_stride, const void* q_weight,
@@ -468,7 +470,7 @@ jt_status jt_qkv_append(const void* qkv, int dtype, int64_t row_stride, const vo
  *   q:        [total_tokens, Hq, D] (dtype), the new tokens' queries.
  *   chunk_off: int32 [nseq+1]: sequence b owns tokens chunk_off[b] ..
  *             chunk_off[b+1]-1, B_b of them, 0 <= B_b <= max_chunk; rows at or
- *             beyond chunk_off[nseq] are neither read nor written.
+ *             beyond chunk_off[nseq] have no effect and are not written.
  *   prefix_len: int32 [nseq], L_b tokens cached before; the new tokens' K/V are
  *             in the slots L_b .. L_b + B_b - 1 (jt_qkv_append puts them
  *             there); L_b + B_b <= max_pages * page_size.
@@ -480,7 +482,13 @@ jt_status jt_qkv_append(const void* qkv, int dtype, int64_t row_stride, const vo
  *             fp32: D in {32, 64, 96, 128}, Hq/Hkv <= 64; else
  *             JT_ERR_UNSUPPORTED.  scale > 0.
  *   out:      [total_tokens, Hq, D] (dtype), lse: fp32 [total_tokens, Hq] or
- *             NULL, as in jt_tree_attn_paged.
+ *             NULL, as in jt_tree_attn_paged.  out does not overlap q
+ *             (JT_ERR_INVALID).
+ * What a token sees that is not finite shows in its output as the formula has
+ * it.  bf16 rows that come out not finite are computed a second time, key by key
+ * (a later token's infinity may have got there): such rows cost about 1 us per 8
+ * keys, and where all rows of a query tile do over some 500000 keys the call can
+ * run into its own time limit (JT_ERR_TIMEOUT).
  * The bf16 path runs on CTA pairs with the key tiles of all (sequence, KV
  * head, query-tile pair) units cut into equal ranges, planned on the device;
  * repeated calls give identical bits.  total_tokens = 0 does nothing.
@@ -505,7 +513,8 @@ jt_status jt_chunk_attn_paged(const void* q, const void* k_cache, const void* v_
  *   k_cache, v_cache: `layers` caches [num_pages, page_size, Hkv, D] (dtype),
  *             layer_stride elements apart (one layer: any value); the block
  *             table serves all layers.  Hkv * D * element size is a multiple
- *             of 16, else JT_ERR_UNSUPPORTED.
+ *             of 16, else JT_ERR_UNSUPPORTED.  k_cache is not v_cache
+ *             (JT_ERR_INVALID).
  *   accept_len, path (int32 [nseq], [nseq, N+1]): jt_verify_accept*'s outputs.
  *   prefix_len, tree_off, block_table: as in jt_tree_attn_paged.
  *   new_prefix: int32 [nseq]; may be prefix_len itself (updated in place).

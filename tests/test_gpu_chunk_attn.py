@@ -143,6 +143,20 @@ def test_a_cut_unit_with_values_that_are_not_finite():
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("prefix,new", [([300], [2]), ([6000], [3]), ([2000], [300])])
+def test_runs_of_keys_that_are_nan(dtype, prefix, new):
+    """Whole key tiles, and whole pieces of a cut unit, whose scores are all NaN, at
+    the front, in the middle and at the end: output and lse of every row are NaN."""
+    L = prefix[0]
+    for first, count in ((0, 256), (L // 2 // 128 * 128, 128), (L // 4, L // 2), (0, L)):
+        s = batch(32, prefix, new, 8, 2, 128, dtype)
+        page, row = slots(s["table"], 0, first, count)
+        s["k"][page, row] = math.nan
+        out, lse = run(s)
+        assert bool(torch.isnan(out).all()) and bool(torch.isnan(lse).all()), (first, count)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 def test_rows_behind_the_last_sequence_stay(dtype):
     s = batch(11, [50, 3], [7, 20], 8, 2, 64, dtype, spare_rows=9)
     out = torch.full_like(s["q"], 5.0)

@@ -158,6 +158,24 @@ def test_append_extremes():
     check_append(s, run_append(s), k0, v0)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_append_infinity_stays_in_its_element(dtype, interleaved):
+    """An infinity among the elements that are not rotated: the norm's factor is
+    0, so its head is 0 but for the NaN that infinity times 0 is, in its own place."""
+    s = append_case(31, [5], [3], 4, 2, 128, dtype, 64, interleaved)
+    s["qkv"] = s["qkv"].contiguous()
+    x = s["qkv"].view(3, 8, 128)
+    for h in (1, 5):  # a query and a key head
+        x[1, h, 99] = math.inf
+    q = run_append(s)
+    page, row = slots(s["table"], 0, 6, 1)
+    for got in (q[1, 1], s["k"][page[0], row[0], 1]):
+        assert bool(torch.isnan(got[99])) and int(torch.isnan(got).sum()) == 1
+        assert bool((got[:99] == 0).all()) and bool((got[100:] == 0).all())
+    assert bool(torch.isfinite(q[[0, 2]]).all()) and bool(torch.isfinite(q[1, [0, 2, 3]]).all())
+
+
 def test_append_skips_and_flags_what_is_out_of_range():
     s = append_case(132, [10, 20, 30], [4, 5, 6], 4, 2, 128, BF16, 128)
     ws = jt.workspace(256)

@@ -100,6 +100,44 @@ def test_commit_refusals(change, status):
     assert call("jt_kv_commit", COMMIT, **change) == status
 
 
+W = ctypes.c_void_p(1 << 40)  # a workspace far from the arrays
+
+
+@pytest.mark.parametrize("a,b", [("qkv", "q_out"), ("qkv", "k_cache"), ("qkv", "v_cache"), ("q_out", "k_cache"),
+                                 ("q_out", "v_cache"), ("k_cache", "v_cache")])
+@pytest.mark.parametrize("shift", [0, 16])
+def test_append_refuses_arrays_that_overlap(a, b, shift):
+    apart = {n: ctypes.c_void_p((i + 1) << 32) for i, n in enumerate(("qkv", "q_out", "k_cache", "v_cache"))}
+    apart[b] = ctypes.c_void_p(apart[a].value + shift)
+    assert call("jt_qkv_append", APPEND, **apart, ws=W, ws_bytes=256) == INVALID
+
+
+@pytest.mark.parametrize("dtype,shift", [(1, 0), (1, 5 * 32 * 128 * 2 - 16), (0, 0), (0, 5 * 32 * 128 * 4 - 16)])
+def test_chunk_refuses_an_output_over_its_queries(dtype, shift):
+    out = ctypes.c_void_p(A.value + shift)
+    assert call("jt_chunk_attn_paged", CHUNK, dtype=dtype, out=out, ws=W, ws_bytes=1 << 34) == INVALID
+
+
+def test_commit_refuses_one_cache_for_keys_and_values():
+    assert call("jt_kv_commit", COMMIT, ws=W, ws_bytes=1 << 20) == INVALID
+
+
+def test_a_longest_chunk_of_any_int_has_a_workspace_size():
+    size = jt.jt_workspace_size
+    big = size(jt.JT_OP_CHUNK_ATTN, 1, 0, 0, 0, 5, 1, 1, 64, 4, (1 << 31) - 1)
+    assert big >= 4096
+
+
+def test_a_stream_of_another_device_is_refused(monkeypatch):
+    class Other:
+        device_index = 1
+
+    monkeypatch.setattr(binding, "_device_of", lambda objs, idx, where: 0)
+    for fn in (jt.jt_qkv_append, jt.jt_chunk_attn_paged, jt.jt_kv_commit):
+        with pytest.raises(ValueError, match="stream on cuda:1"):
+            fn(None, stream=Other())
+
+
 def test_workspace_sizes():
     size = jt.jt_workspace_size
     assert size(jt.JT_OP_QKV_APPEND) == 256

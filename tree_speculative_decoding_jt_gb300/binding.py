@@ -615,6 +615,9 @@ def _on_given_stream(fn):
     def wrapper(*args, stream=None, **kwargs):
         if stream is None:
             return fn(*args, **kwargs)
+        idx = _device_of(kwargs.values(), _device_of(args, -1, fn.__name__), fn.__name__)
+        if idx >= 0 and stream.device_index != idx:
+            raise ValueError(f"{fn.__name__}: tensors on cuda:{idx}, stream on cuda:{stream.device_index}")
         with torch.cuda.stream(stream):
             return fn(*args, **kwargs)
     return wrapper

@@ -300,7 +300,7 @@ __device__ void plan_slot(const Params& p, Bars* bars, int lane, int work, int n
         total += warp_sum(t);
         units += warp_sum(u);
     }
-    if (total > 0x7FFFFFFFll) {  // beyond the int tile arithmetic: refuse the launch's work
+    if (total > 0x7FFF0000ll) {  // beyond the int tile arithmetic: refuse the launch's work
         if (rec && lane == 0) raise_error(p.err, DEVERR_INVALID);
         total = 0;
     }
@@ -594,15 +594,13 @@ __device__ __forceinline__ void stage_store(uint8_t* stage, int lane, const uint
 // the values of a chunk's later token reach the rows before it in the same key
 // tile.  A row that comes out not finite is computed again here, key by key over
 // the keys that it sees (a warp per row): rare, and then right.
-// Columns [c0, c0 + 32 * kPer) of the row's output.
 // ---------------------------------------------------------------------------
-template <int D, int kPer>
-__device__ __noinline__ void redo_row(const Params& p, int b, int L, int g, int token, long long rowid, int c0,
-                                      int lane) {
-    constexpr int kQ = D / 32;
-    float qv[kQ], acc[kPer];
+template <int D>
+__device__ __noinline__ void redo_row(const Params& p, int b, int L, int g, int token, long long rowid, int lane) {
+    constexpr int kPer = D / 32;
+    float qv[kPer], acc[kPer];
 #pragma unroll
-    for (int k = 0; k < kQ; ++k) qv[k] = __bfloat162float(p.q[rowid * D + lane + 32 * k]);
+    for (int k = 0; k < kPer; ++k) qv[k] = __bfloat162float(p.q[rowid * D + lane + 32 * k]);
 #pragma unroll
     for (int k = 0; k < kPer; ++k) acc[k] = 0.0f;
     float m = -INFINITY, l = 0.0f;
@@ -619,11 +617,11 @@ __device__ __noinline__ void redo_row(const Params& p, int b, int L, int g, int 
             d[i] = 0.0f;
             const bool on = in_pool && i < n;
 #pragma unroll
-            for (int k = 0; k < kQ; ++k)
+            for (int k = 0; k < kPer; ++k)
                 d[i] = fmaf(qv[k], on ? __bfloat162float(p.k_cache[base + i * step + lane + 32 * k]) : 0.0f, d[i]);
 #pragma unroll
             for (int k = 0; k < kPer; ++k)
-                v[i][k] = on ? __bfloat162float(p.v_cache[base + i * step + c0 + lane + 32 * k]) : 0.0f;
+                v[i][k] = on ? __bfloat162float(p.v_cache[base + i * step + lane + 32 * k]) : 0.0f;
         }
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1)
@@ -644,7 +642,7 @@ __device__ __noinline__ void redo_row(const Params& p, int b, int L, int g, int 
     }
     const float inv = 1.0f / l;
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) p.out[rowid * D + c0 + lane + 32 * k] = __float2bfloat16(acc[k] * inv);
+    for (int k = 0; k < kPer; ++k) p.out[rowid * D + lane + 32 * k] = __float2bfloat16(acc[k] * inv);
 }
 
 // Operand descriptors are stepped by adding the byte offset / 16 to the
@@ -802,8 +800,9 @@ __device__ __noinline__ void merge_rows(const Params& p, const Piece& pc, const 
                 for (int k = 0; k < K; ++k) {
                     const float mk = __shfl_sync(0xFFFFFFFFu, ml.x, i * K + k);
                     const float lk = __shfl_sync(0xFFFFFFFFu, ml.y, i * K + k);
-                    // a piece without a visible key has weight 0, and O that says nothing
-                    if (mk != -INFINITY) {
+                    // a piece without a visible key has weight 0, and O that says nothing;
+                    // one whose scores are all NaN has m = -inf too, and a NaN sum
+                    if (lk != 0.0f) {
                         const float w = exp2f(mk - mi);
                         lsum[i] += w * lk;
 #pragma unroll
@@ -833,7 +832,7 @@ __device__ __noinline__ void merge_rows(const Params& p, const Piece& pc, const 
             if (lane == 0 && p.lse) p.lse[rowid] = (M[i] + log2f(lsum[i])) * 0.6931471805599453f;
             if (lsum[i] == lsum[i] && __any_sync(0xFFFFFFFFu, probe != 0.0f)) {
                 __syncwarp();
-                redo_row<D, kC>(p, pc.b, pc.s.L, pc.g, token, rowid, 0, lane);
+                redo_row<D>(p, pc.b, pc.s.L, pc.g, token, rowid, lane);
             }
         }
     }
@@ -1179,7 +1178,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         }
                         tell_partner(t, m_run);
                     }
-                    if (m_before != m_run) l_run = m_before == -INFINITY ? 0.0f : l_run * ex2_approx(m_before - m_run);
+                    if (m_before != m_run) l_run = l_run == 0.0f ? 0.0f : l_run * ex2_approx(m_before - m_run);
                     l_run += sum;
                     tmem_wait_st();
                 } else {
@@ -1257,8 +1256,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const float2 xa = xch[(npc % kRing) * 256], xb = xch[(npc % kRing) * 256 + 128];
             ++npc;
             const float m_tot = fmaxf(xa.x, xb.x);
-            const float l_tot = (xa.x == -INFINITY ? 0.0f : xa.y * ex2_approx(xa.x - m_tot)) +
-                                (xb.x == -INFINITY ? 0.0f : xb.y * ex2_approx(xb.x - m_tot));
+            // (a sum is 0 without a key, and NaN beside m = -inf where every score was NaN: it stays NaN)
+            const float l_tot = (xa.y == 0.0f ? 0.0f : xa.y * ex2_approx(xa.x - m_tot)) +
+                                (xb.y == 0.0f ? 0.0f : xb.y * ex2_approx(xb.x - m_tot));
             if (ws->w.remaining <= 0) pdl_trigger();
             if (!mbar_wait_warp(&bars->o_done[last % 3], (last / 3) & 1, p.err, abort)) break;
             tc_fence_after();
@@ -1319,8 +1319,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     const int rr = __ffs(bad) - 1;
                     bad &= bad - 1;
                     __syncwarp();
-                    redo_row<D, D / 32>(p, pc.b, pc.s.L, pc.g, __shfl_sync(0xFFFFFFFFu, token, rr),
-                                        __shfl_sync(0xFFFFFFFFu, rowid, rr), 0, lane);
+                    redo_row<D>(p, pc.b, pc.s.L, pc.g, __shfl_sync(0xFFFFFFFFu, token, rr),
+                                        __shfl_sync(0xFFFFFFFFu, rowid, rr), lane);
                 }
             }
             if (partial && tile_on) {

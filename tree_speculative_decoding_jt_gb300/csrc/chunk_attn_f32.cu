@@ -322,7 +322,7 @@ struct Plan {
 static Plan plan(int nseq, int Hq, int Hkv, int max_pages, int max_chunk) {
     Plan pl;
     pl.npt = std::max(1, kRows / (Hq / Hkv));
-    pl.mtiles = (max_chunk + pl.npt - 1) / pl.npt;
+    pl.mtiles = (max_chunk - 1) / pl.npt + 1;  // max_chunk may be INT_MAX
     pl.units = static_cast<long long>(nseq) * Hkv * pl.mtiles;
     const long long tmax = (static_cast<long long>(max_pages) * JT_PAGE_SIZE + kKeys - 1) / kKeys;
     const long long want = 16ll * std::max(1, device_sm_count()) / std::max(1ll, pl.units);

@@ -32,6 +32,11 @@ static jt_status from_cuda(cudaError_t e) {
 
 static bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+static bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return na > 0 && nb > 0 && x < y + static_cast<uintptr_t>(nb) && y < x + static_cast<uintptr_t>(na);
+}
+
 static jt_status check_ws(void* ws, size_t ws_bytes, size_t need) {
     if (!ws || !aligned(ws, kAlign) || ws_bytes < need) return JT_ERR_WORKSPACE;
     return JT_OK;
@@ -329,6 +334,12 @@ jt_status jt_qkv_append(const void* qkv, int dtype, int64_t row_stride, const vo
         return JT_ERR_INVALID;
     jt_status s = check_ws(ws, ws_bytes, kWsHeader);
     if (s != JT_OK) return s;
+    const int64_t esize = bf16 ? 2 : 4, pool = static_cast<int64_t>(num_pages) * JT_PAGE_SIZE * Hkv * D * esize;
+    const int64_t in = (static_cast<int64_t>(total_nodes - 1) * row_stride + (Hq + 2ll * Hkv) * D) * esize;
+    const int64_t qb = static_cast<int64_t>(total_nodes) * Hq * D * esize;
+    if (overlap(k_cache, pool, v_cache, pool) || overlap(qkv, in, k_cache, pool) || overlap(qkv, in, v_cache, pool) ||
+        overlap(q_out, qb, k_cache, pool) || overlap(q_out, qb, v_cache, pool) || overlap(q_out, qb, qkv, in))
+        return JT_ERR_INVALID;
     AppendArgs a;
     a.qkv = qkv;
     a.q_weight = q_weight;
@@ -383,6 +394,8 @@ jt_status jt_chunk_attn_paged(const void* q, const void* k_cache, const void* v_
                            bf16 ? chunk_attn_bf16_workspace_bytes(D)
                                 : chunk_attn_f32_workspace_bytes(nseq, Hq, Hkv, D, max_pages, max_chunk));
     if (s != JT_OK) return s;
+    const int64_t bytes = static_cast<int64_t>(total_tokens) * Hq * D * (bf16 ? 2 : 4);
+    if (overlap(q, bytes, out, bytes)) return JT_ERR_INVALID;  // other CTAs may still read the queries of a row written
     ChunkArgs a;
     a.q = q;
     a.k_cache = k_cache;
@@ -424,12 +437,12 @@ jt_status jt_kv_commit(void* k_cache, void* v_cache, int dtype, int layers, int6
                        layer_stride * esize % 16 != 0))
         return JT_ERR_INVALID;
     if (!aligned(k_cache, 16) || !aligned(v_cache, 16)) return JT_ERR_INVALID;
-    const uintptr_t x = reinterpret_cast<uintptr_t>(new_prefix), y = reinterpret_cast<uintptr_t>(prefix_len);
-    const uintptr_t n = static_cast<uintptr_t>(nseq) * sizeof(int32_t);
-    const bool in_place = x == y;
-    if (!in_place && x < y + n && y < x + n) return JT_ERR_INVALID;  // partly overlapping
+    const int64_t n = static_cast<int64_t>(nseq) * static_cast<int64_t>(sizeof(int32_t));
+    const bool in_place = new_prefix == prefix_len;
+    if (!in_place && overlap(new_prefix, n, prefix_len, n)) return JT_ERR_INVALID;
     jt_status s = check_ws(ws, ws_bytes, in_place ? kv_commit_workspace_bytes(nseq) : kWsHeader);
     if (s != JT_OK) return s;
+    if (k_cache == v_cache) return JT_ERR_INVALID;  // two CTAs would move the same path
     CommitArgs a;
     a.k_cache = k_cache;
     a.v_cache = v_cache;

@@ -249,9 +249,11 @@ __global__ void __launch_bounds__(kAppendThreads) qkv_append_kernel(const Append
                 for (int j = 0; j < N; j += 2) {
                     float x0, x1, y0, y1;
                     mul2(x0, x1, fa[j], fa[j + 1], ca[j], ca[j + 1]);
-                    fma2(x0, x1, fb[j], fb[j + 1], sb[j], sb[j + 1], x0, x1);
                     mul2(y0, y1, fb[j], fb[j + 1], cb[j], cb[j + 1]);
-                    fma2(y0, y1, fa[j], fa[j + 1], sa[j], sa[j + 1], y0, y1);
+                    if (rotated) {  // elsewhere 0 times an infinity would reach the neighbour
+                        fma2(x0, x1, fb[j], fb[j + 1], sb[j], sb[j + 1], x0, x1);
+                        fma2(y0, y1, fa[j], fa[j + 1], sa[j], sa[j + 1], y0, y1);
+                    }
                     mul2(fa[j], fa[j + 1], x0, x1, inv, inv);
                     mul2(fb[j], fb[j + 1], y0, y1, inv, inv);
                 }
@@ -283,8 +285,9 @@ static cudaError_t append_launch(Append prm, cudaStream_t st) {
     const long long warps = static_cast<long long>(prm.total) * prm.warps_per_token;
     const long long blocks = (warps + kAppendThreads / 32 - 1) / (kAppendThreads / 32);
     if (blocks > 0x7FFFFFFFll) return cudaErrorInvalidValue;
-    return launch_kernel_pdl(prm.interleaved ? qkv_append_kernel<T, D, LPH, true> : qkv_append_kernel<T, D, LPH, false>, dim3(static_cast<unsigned>(blocks)), dim3(kAppendThreads), 0,
-                             st, prm);
+    return launch_kernel_pdl(
+        prm.interleaved ? qkv_append_kernel<T, D, LPH, true> : qkv_append_kernel<T, D, LPH, false>,
+        dim3(static_cast<unsigned>(blocks)), dim3(kAppendThreads), 0, st, prm);
 }
 
 // ---------------------------------------------------------------------------
