@@ -741,99 +741,163 @@ __device__ __forceinline__ int bt_group(const Params& p, const Piece& pc, int va
                : 0;
 }
 
-// Merge of a cut unit's pieces for this CTA's query tile x.  Rows are dealt to
-// the 4 epilogue warps, R at a time; per row M = max m_k, O = sum_k 2^(m_k - M)
-// O_k / sum_k 2^(m_k - M) l_k, in piece order whoever merges, so every call
-// rounds the same way.  R x K partial rows are in flight: many rows of few
-// pieces (prompts) or few rows of many (single tokens).
-template <int D, int R, int K>
-__device__ __noinline__ void merge_rows(const Params& p, const Piece& pc, const CutUnit cu, int x, int swarp,
-                                        int lane) {
-    static_assert(R * K <= 32, "one (row, piece) per lane");
-    constexpr int kC = D / 32;  // columns per lane
-    const int tok0 = (2 * pc.mp + x) * p.npt;
-    const int rows = min(pc.s.B - tok0, p.npt) * p.G;
-    const int sub = lane % K, rsub = (lane / K) % R;  // lane = (row of the batch, piece of the group)
-    const long long stride = static_cast<long long>(2) * kTileM;  // between partial slots
-    for (int r0 = swarp * R; r0 < rows; r0 += 4 * R) {
-        const long long xr = static_cast<long long>(x) * kTileM + min(r0 + rsub, rows - 1);
-        float M[R], lsum[R], acc[R][kC];
+// Merge of a cut unit's pieces for this CTA's query tile x, by the 4 epilogue
+// warps.  Per row M = max m_k, O = sum_k 2^(m_k - M) O_k / sum_k 2^(m_k - M) l_k,
+// in piece order whoever merges, so every call rounds the same way.  A piece
+// without a visible key has l = 0 and an O that says nothing; one whose scores
+// are all NaN has m = -inf and a NaN sum, which stays.  Both forms are small
+// loops: a merge runs once or twice in a CTA's life, from a cold instruction
+// cache (16 sequences of 1 to 512 tokens on 1024 to 8192, 32/8 heads, D 128: 216
+// us with rows and pieces unrolled, 199 so).
+template <int kC>
+__device__ __forceinline__ void load_cols(const float* src, float (&v)[kC]) {
+    if constexpr (kC == 4) {
+        const float4 f = __ldcg(reinterpret_cast<const float4*>(src));
+        v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
+    } else {
+        const float2 f = __ldcg(reinterpret_cast<const float2*>(src));
+        v[0] = f.x, v[1] = f.y;
+    }
+}
+// The row's columns to dst as bf16; whether some are not finite (warp-uniform).
+template <int kC>
+__device__ __forceinline__ bool store_cols(__nv_bfloat16* dst, const float (&acc)[kC], float inv) {
+    float o[kC], probe = 0.0f;
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-            M[i] = -INFINITY;
-            lsum[i] = 0.0f;
+    for (int c = 0; c < kC; ++c) {
+        o[c] = acc[c] * inv;
+        probe += o[c] * 0.0f;
+    }
+    if (dst) {
+        if constexpr (kC == 4)
+            *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
+        else
+            *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(o[0], o[1]);
+    }
+    return __any_sync(0xFFFFFFFFu, probe != 0.0f);
+}
+
+// More rows than pieces (prompts): a warp takes up to 32 rows, 8 of them at a
+// time; lane i keeps the weights of its row i.
+template <int D>
+__device__ __noinline__ void merge_many(const Params& p, const Piece& pc, const CutUnit cu, int x, int rows, int swarp,
+                                        int lane) {
+    constexpr int kC = D / 32;               // columns per lane
+    const int q = (rows + 31) / 32 * 8;      // rows per warp
+    const int base = swarp * q, n = min(rows - base, q);
+    if (n <= 0) return;
+    const int r = min(base + lane, rows - 1);  // this lane's row
+    const int token = (2 * pc.mp + x) * p.npt + r / p.G;
+    const long long rowid = static_cast<long long>(pc.s.off + token) * p.Hq + pc.g * p.G + r % p.G;
+    constexpr long long stride = 2ll * kTileM;  // rows between partial slots
+    const float2* ml = p.part_ml + x * kTileM + r;
+    float M = -INFINITY, l = 0.0f;
+#pragma unroll 2
+    for (int k = 0; k < cu.n; ++k) M = fmaxf(M, __ldcg(ml + cu.slot(k) * stride).x);
+#pragma unroll 2
+    for (int k = 0; k < cu.n; ++k) {
+        const float2 a = __ldcg(ml + cu.slot(k) * stride);
+        l += a.y == 0.0f ? 0.0f : exp2f(a.x - M) * a.y;
+    }
+    const float inv = 1.0f / l;
+    if (p.lse && lane < n) p.lse[rowid] = (M + log2f(l)) * 0.6931471805599453f;
+    unsigned bad = 0u;
+#pragma unroll 1
+    for (int r0 = 0; r0 < n; r0 += 8) {
+        const float* src = p.part_o + (x * kTileM + base + r0) * D + lane * kC;
+        float acc[8][kC];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
 #pragma unroll
             for (int c = 0; c < kC; ++c) acc[i][c] = 0.0f;
-        }
 #pragma unroll 1
-        for (int k0 = 0; k0 < cu.n; k0 += K) {
-            const float2 ml = k0 + sub < cu.n ? __ldcg(&p.part_ml[cu.slot(k0 + sub) * stride + xr])
-                                              : make_float2(-INFINITY, 0.0f);
-            float v[R][K][kC];
+        for (int k = 0; k < cu.n; ++k) {
+            const long long at = cu.slot(k) * stride;
+            const float2 a = __ldcg(ml + at);
+            float v[8][kC];
 #pragma unroll
-            for (int i = 0; i < R; ++i)
+            for (int i = 0; i < 8; ++i) load_cols<kC>(src + at * D + i * D, v[i]);
+            const float w = a.y == 0.0f ? 0.0f : exp2f(a.x - M);
 #pragma unroll
-                for (int k = 0; k < K; ++k) {
-                    const float* src = p.part_o +
-                                       (cu.slot(min(k0 + k, cu.n - 1)) * stride + x * kTileM + min(r0 + i, rows - 1)) * D +
-                                       lane * kC;
-                    if constexpr (kC == 4) {
-                        const float4 f = __ldcg(reinterpret_cast<const float4*>(src));
-                        v[i][k][0] = f.x, v[i][k][1] = f.y, v[i][k][2] = f.z, v[i][k][3] = f.w;
-                    } else {
-                        const float2 f = __ldcg(reinterpret_cast<const float2*>(src));
-                        v[i][k][0] = f.x, v[i][k][1] = f.y;
-                    }
-                }
-            float mx = ml.x;  // the group's maximum of this lane's row
+            for (int i = 0; i < 8; ++i) {
+                const float wi = __shfl_sync(0xFFFFFFFFu, w, r0 + i);
+                if (wi != 0.0f)
 #pragma unroll
-            for (int o = K / 2; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
-#pragma unroll
-            for (int i = 0; i < R; ++i) {
-                const float mi = fmaxf(M[i], __shfl_sync(0xFFFFFFFFu, mx, i * K));
-                const float old = M[i] == -INFINITY ? 0.0f : exp2f(M[i] - mi);  // what earlier groups are worth now
-                M[i] = mi;
-                lsum[i] *= old;
-#pragma unroll
-                for (int c = 0; c < kC; ++c) acc[i][c] *= old;
-#pragma unroll
-                for (int k = 0; k < K; ++k) {
-                    const float mk = __shfl_sync(0xFFFFFFFFu, ml.x, i * K + k);
-                    const float lk = __shfl_sync(0xFFFFFFFFu, ml.y, i * K + k);
-                    // a piece without a visible key has weight 0, and O that says nothing;
-                    // one whose scores are all NaN has m = -inf too, and a NaN sum
-                    if (lk != 0.0f) {
-                        const float w = exp2f(mk - mi);
-                        lsum[i] += w * lk;
-#pragma unroll
-                        for (int c = 0; c < kC; ++c) acc[i][c] += w * v[i][k][c];
-                    }
-                }
+                    for (int c = 0; c < kC; ++c) acc[i][c] = fmaf(wi, v[i][c], acc[i][c]);
             }
         }
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-            const int r = r0 + i;
-            if (r >= rows) continue;
-            const int token = tok0 + r / p.G;
-            const long long rowid = static_cast<long long>(pc.s.off + token) * p.Hq + pc.g * p.G + r % p.G;
-            const float inv = 1.0f / lsum[i];
-            float o[kC], probe = 0.0f;
+        for (int i = 0; i < 8; ++i) {
+            const long long id = __shfl_sync(0xFFFFFFFFu, rowid, r0 + i);
+            const bool nf = store_cols<kC>(r0 + i < n ? p.out + id * D + lane * kC : nullptr, acc[i],
+                                           __shfl_sync(0xFFFFFFFFu, inv, r0 + i));
+            if (nf && r0 + i < n) bad |= 1u << (r0 + i);
+        }
+    }
+    bad &= __ballot_sync(0xFFFFFFFFu, l == l);
+    while (bad) {
+        const int i = __ffs(bad) - 1;
+        bad &= bad - 1;
+        __syncwarp();
+        redo_row<D>(p, pc.b, pc.s.L, pc.g, __shfl_sync(0xFFFFFFFFu, token, i), __shfl_sync(0xFFFFFFFFu, rowid, i), lane);
+    }
+}
+
+// More pieces than rows (single tokens): a warp takes one row at a time, 32
+// pieces' weights in its lanes and 16 pieces' O in flight.
+template <int D>
+__device__ __noinline__ void merge_few(const Params& p, const Piece& pc, const CutUnit cu, int x, int rows, int swarp,
+                                       int lane) {
+    constexpr int kC = D / 32, kBatch = 16;
+    constexpr long long stride = 2ll * kTileM;
+#pragma unroll 1
+    for (int r = swarp; r < rows; r += 4) {
+        const long long xr = x * kTileM + r;
+        const int token = (2 * pc.mp + x) * p.npt + r / p.G;
+        const long long rowid = static_cast<long long>(pc.s.off + token) * p.Hq + pc.g * p.G + r % p.G;
+        float M = -INFINITY, l = 0.0f, acc[kC];
 #pragma unroll
-            for (int c = 0; c < kC; ++c) {
-                o[c] = acc[i][c] * inv;
-                probe += o[c] * 0.0f;
+        for (int c = 0; c < kC; ++c) acc[c] = 0.0f;
+#pragma unroll 1
+        for (int k0 = 0; k0 < cu.n; k0 += 32) {
+            const float2 a = k0 + lane < cu.n ? __ldcg(p.part_ml + cu.slot(k0 + lane) * stride + xr)
+                                              : make_float2(-INFINITY, 0.0f);
+            float w = 0.0f;
+#pragma unroll 1
+            for (int kk = k0; kk < min(cu.n, k0 + 32); kk += kBatch) {
+                float v[kBatch][kC];
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k)
+                    load_cols<kC>(p.part_o + (cu.slot(min(kk + k, cu.n - 1)) * stride + xr) * D + lane * kC, v[k]);
+                if (kk == k0) {
+                    float mx = a.x, sum;
+#pragma unroll
+                    for (int o = 16; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
+                    mx = fmaxf(mx, M);
+                    const float old = l == 0.0f ? 0.0f : exp2f(M - mx);  // what earlier pieces are worth now
+                    M = mx;
+                    w = a.y == 0.0f ? 0.0f : exp2f(a.x - mx);
+                    sum = w * a.y;
+#pragma unroll
+                    for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+                    l = l * old + sum;
+#pragma unroll
+                    for (int c = 0; c < kC; ++c) acc[c] *= old;
+                }
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+                    const float wk = __shfl_sync(0xFFFFFFFFu, w, (kk - k0 + k) & 31);
+                    if (wk != 0.0f)  // past the last piece, too
+#pragma unroll
+                        for (int c = 0; c < kC; ++c) acc[c] = fmaf(wk, v[k][c], acc[c]);
+                }
             }
-            __nv_bfloat16* dst = p.out + rowid * D + lane * kC;
-            if constexpr (kC == 4)
-                *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
-            else
-                *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(o[0], o[1]);
-            if (lane == 0 && p.lse) p.lse[rowid] = (M[i] + log2f(lsum[i])) * 0.6931471805599453f;
-            if (lsum[i] == lsum[i] && __any_sync(0xFFFFFFFFu, probe != 0.0f)) {
-                __syncwarp();
-                redo_row<D>(p, pc.b, pc.s.L, pc.g, token, rowid, lane);
-            }
+        }
+        const bool nf = store_cols<kC>(p.out + rowid * D + lane * kC, acc, 1.0f / l);
+        if (lane == 0 && p.lse) p.lse[rowid] = (M + log2f(l)) * 0.6931471805599453f;
+        if (nf && l == l) {
+            __syncwarp();
+            redo_row<D>(p, pc.b, pc.s.L, pc.g, token, rowid, lane);
         }
     }
 }
@@ -1343,12 +1407,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
                 if (!meet4(1)) break;
                 if (bars->merge_flag) {
-                    if (cu.n <= 2)
-                        merge_rows<D, 8, 2>(p, pc, cu, x, w4, lane);
-                    else if (cu.n <= 8)
-                        merge_rows<D, 2, 8>(p, pc, cu, x, w4, lane);
+                    const int rows = min(pc.s.B - tok0, npt) * p.G;
+                    if (rows > cu.n)
+                        merge_many<D>(p, pc, cu, x, rows, w4, lane);
                     else
-                        merge_rows<D, 1, 16>(p, pc, cu, x, w4, lane);
+                        merge_few<D>(p, pc, cu, x, rows, w4, lane);
                 }
             }
         }
