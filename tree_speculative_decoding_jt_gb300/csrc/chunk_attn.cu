@@ -45,6 +45,20 @@
 // TMEM (512 columns): S0, S1, S2 (P of a tile overwrites the first half of its
 // S) and O.  S runs up to three tiles ahead of O, across units; Q is double
 // buffered.
+//
+// What bounds it, measured (32/8 heads, D 128 unless said; flops of the visible
+// (token, key) pairs, bytes read and written once):
+//   8192 tokens on 8192           1120-1160 us, 1.42-1.47 PFLOP/s: the chain score
+//     -> softmax -> P -> output MMA of a tile over three S buffers (1650 cycles a
+//     tile where its MMAs take 1080);
+//   16 sequences, 1 to 512 tokens on 1024 to 8192   199 us, 1.0 PFLOP/s: the same,
+//     0.11 of the work past the chunks' ends, and some 2.5 us a piece;
+//   32 single tokens on 32768     650 us, 6.6 TB/s: HBM;
+//   1 token on 4096               18.6 us: latency (plan, 3 or 4 tiles, merge);
+//   D 64, 5 chunks of up to 1500  106 us: exponentials and pieces.
+// A tile's row maximum taken by the TMEM load itself, P released in halves, the
+// exponential as a polynomial, scores in halves of 64 keys, and the piece cut by a
+// range's end done first (its merge then amid the others) were slower or equal.
 #include <algorithm>
 
 #include "jt_common.cuh"
@@ -277,7 +291,7 @@ __device__ __forceinline__ int padded_head_tiles(const SeqInfo& s, int npt, int 
 // units (at most half the slots) every unit starts at a range's start instead, P
 // being large enough for the units' last ranges to be cut short: a slot then
 // has one piece, and no slot the ends of two units one after the other (one
-// token over 4096, 8 KV heads: 24 -> 20 us).  rec: also report the sequences
+// token over 4096, 8 KV heads: 24 -> 19 us).  rec: also report the sequences
 // whose offsets or lengths are out of range.
 __device__ void plan_slot(const Params& p, Bars* bars, int lane, int work, int nwork, bool rec) {
     SeqInfo mine;  // the sequence of this lane in the batch's last 32

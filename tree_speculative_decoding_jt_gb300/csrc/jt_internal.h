@@ -37,7 +37,7 @@ inline size_t align_up(size_t n) { return (n + kAlign - 1) / kAlign * kAlign; }
 struct WsHeader {
     uint32_t err;                // device error flags (DEVERR_*)
     uint32_t arrivals;           // kv_commit: CTAs of the running call that have read their lengths (0 between calls)
-    unsigned long long tickets;  // attention: CTA arrivals over all calls (call number = tickets / grid)
+    unsigned long long tickets;  // attentions: CTA arrivals over all calls, from which a call has its number
 };
 constexpr size_t kWsHeader = kAlign;
 

