@@ -77,10 +77,18 @@ constexpr int kSoftmaxRegs = 136, kEpilogueRegs = 160, kOtherRegs = 80;
 static_assert(kSoftmaxRegs >= kLaunchRegs && kEpilogueRegs >= kLaunchRegs && kOtherRegs <= kLaunchRegs);
 static_assert(kSoftmaxRegs % 8 == 0 && kEpilogueRegs % 8 == 0 && kOtherRegs % 8 == 0);
 static_assert(256 * kSoftmaxRegs + 128 * kEpilogueRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs);
-constexpr int kRing = 4;     // pieces whose rows' sums may wait for the epilogue
 constexpr int kTileN = 128;  // keys per KV tile
 constexpr int kTileM = 128;  // query rows per query tile
 constexpr float kRescaleLog2 = 32.0f;
+// Pieces whose rows' maxima and sums may wait for the epilogue.  A softmax warp
+// writes its entry of piece n once it is through its own tiles, and in a piece of
+// one tile one of the two warps of a row has none.  Tiles alternate, so the last
+// tile that it has seen is at least the one before n's last, no earlier than the
+// last tile e of piece n - 1.  S of that tile waited for the PV three tiles before,
+// which lies in piece n - 4 or later (a piece has at least one tile), and the first
+// PV of piece n - 4 waited until the epilogue had read piece n - 5.  So a warp is at
+// most four pieces ahead of what the epilogue has read: five entries.
+constexpr int kRing = 5;
 
 struct Params {
     const int32_t* block_table;
@@ -1286,9 +1294,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (!ok) break;
             cnt += nt;
             fin += jfin < nt ? 1 : 0;
-            // The rows' maxima and sums go to the epilogue.  Neither warpgroup is
-            // more than three pieces ahead of it: a tile's S waits for the PV
-            // three tiles before, and a piece's first PV for the epilogue.
+            // The rows' maxima and sums go to the epilogue, which has read the
+            // entry's previous piece (see kRing).
             xch[(npc % kRing) * 256] = make_float2(m_run, l_run);
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars->x_bar[npc % kRing][w4]);
