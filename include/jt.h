@@ -484,6 +484,9 @@ jt_status jt_qkv_append(const void* qkv, int dtype, int64_t row_stride, const vo
  *   out:      [total_tokens, Hq, D] (dtype), lse: fp32 [total_tokens, Hq] or
  *             NULL, as in jt_tree_attn_paged.  out does not overlap q
  *             (JT_ERR_INVALID).
+ * A page outside the pool among those a sequence's tokens see raises
+ * JT_ERR_INVALID (device-side); its keys and values are taken as zeros, so what
+ * the sequence's rows hold then says nothing.  Other sequences are not touched.
  * What a token sees that is not finite shows in its output as the formula has
  * it.  bf16 rows that come out not finite are computed a second time, key by key
  * (a later token's infinity may have got there): such rows cost about 1 us per 8

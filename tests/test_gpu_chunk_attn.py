@@ -369,3 +369,28 @@ def test_graphs_that_share_a_workspace_and_a_given_stream(dtype):
     torch.cuda.current_stream().wait_stream(st)
     for g, w in zip(got, want * 2):
         assert torch.equal(g[0], w[0]) and torch.equal(g[1], w[1])
+
+
+@pytest.mark.parametrize("dtype,D", [(BF16, 128), (BF16, 64), (F32, 64)])
+def test_a_page_outside_the_pool_is_reported(dtype, D):
+    """In a sequence's first, middle and last page, for a token and for a prompt; the
+    other sequences' rows are right, and entries that no token sees stay unread."""
+    s = batch(41, [50, 300, 0, 7], [4, 1, 200, 1], 8, 2, D, dtype, max_pages=24)
+    ref, _, A, S = chunk_ref(s)
+    e_out, _ = chunk_bounds(s, ref, A, S)
+    ws = workspace(s)
+    run(s, ws)
+    table = s["table"].clone()
+    for b, page in ((0, 1), (0, 3), (1, 0), (1, 18), (2, 7), (2, 12), (3, 0)):
+        for bad in (-1, s["k"].shape[0], (1 << 31) - 1, -(1 << 31)):
+            s["table"] = table.clone()
+            s["table"][b, page] = bad
+            out, _ = jt.jt_chunk_attn_paged(s["q"], s["k"], s["v"], s["table"], s["L"], s["off"], max_chunk=200, ws=ws)
+            with pytest.raises(jt.JtError) as e:
+                jt.jt_check(ws)
+            assert e.value.status == jt.JT_ERR_INVALID
+            keep = torch.ones(s["total"], dtype=torch.bool, device="cuda")
+            keep[int(s["off"][b]):int(s["off"][b + 1])] = False
+            assert bool(((out.double() - ref).abs()[keep] <= e_out[keep]).all())
+    s["table"] = table
+    check(s, *run(s, ws))

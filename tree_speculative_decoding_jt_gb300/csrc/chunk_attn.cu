@@ -763,6 +763,12 @@ __device__ __forceinline__ int bt_group(const Params& p, const Piece& pc, int va
                : 0;
 }
 
+// A page id, or the first one past the pool for every id outside it: the copies
+// then read zeros, and the K producer reports it.
+__device__ __forceinline__ int page_in_pool(const Params& p, int pid) {
+    return static_cast<int>(min(static_cast<uint32_t>(pid), static_cast<uint32_t>(p.num_pages)));
+}
+
 // Merge of a cut unit's pieces for this CTA's query tile x, by the 4 epilogue
 // warps.  Per row M = max m_k, O = sum_k 2^(m_k - M) O_k / sum_k 2^(m_k - M) l_k,
 // in piece order whoever merges, so every call rounds the same way.  A piece
@@ -1027,8 +1033,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                     const int nvalid = min(kTileN, valid_end - (pc.t0 + j) * kTileN);
                     const int npg = (nvalid + JT_PAGE_SIZE - 1) / JT_PAGE_SIZE;
-                    const int pid = __shfl_sync(0xFFFFFFFFu, bt_cur, ((j & 3) << 3) + (lane & 7));
-                    JT_DCHECK(lane >= npg || (pid >= 0 && pid < p.num_pages), p.err);  // block-table entry in the pool
+                    const int pid = page_in_pool(p, __shfl_sync(0xFFFFFFFFu, bt_cur, ((j & 3) << 3) + (lane & 7)));
+                    if (lane < npg && pid == p.num_pages) raise_error(p.err, DEVERR_INVALID);
                     // this CTA's 64 keys (pages 4X..4X+3 of the tile); the slot frees once QK of tile jj - KS is done
                     if (jj >= KS && !mbar_wait_warp(&bars->k_empty[st], ((jj / KS) & 1) ^ 1, p.err, abort)) {
                         ok = false;
@@ -1073,7 +1079,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                     const int nvalid = min(kTileN, valid_end - (pc.t0 + j) * kTileN);
                     const int npg = (nvalid + JT_PAGE_SIZE - 1) / JT_PAGE_SIZE;
-                    const int pid = __shfl_sync(0xFFFFFFFFu, bt_cur, ((j & 3) << 3) + (lane & 7));
+                    const int pid = page_in_pool(p, __shfl_sync(0xFFFFFFFFu, bt_cur, ((j & 3) << 3) + (lane & 7)));
                     // this CTA's D / 2 dims of every key; the slot frees once PV of tile jj - VS is done
                     if (jj >= VS && !mbar_wait_warp(&bars->v_empty[st], ((jj / VS) & 1) ^ 1, p.err, abort)) {
                         ok = false;
