@@ -110,7 +110,9 @@ typedef enum { JT_OP_TREE_BUILD = 0, JT_OP_TREE_ATTN = 1, JT_OP_VERIFY_ACCEPT = 
  *   TREE_ATTN:     nseq, total_nodes, Hq, Hkv, D, max_pages, max_tree
  *   VERIFY_ACCEPT: nseq, total_nodes
  *   CHUNK_ATTN:    nseq, total_nodes (tokens), Hq, Hkv, D, max_pages,
- *                  max_tree (the longest chunk); enough for either dtype
+ *                  max_tree (the longest chunk); enough for either dtype and
+ *                  for every call with at most these sequences, pages and
+ *                  chunk lengths.  bf16 needs the size for max_pages = 1
  *   KV_COMMIT:     nseq
  *   QKV_APPEND:    (256 bytes: the header only)
  */
@@ -496,9 +498,13 @@ jt_status jt_qkv_append(const void* qkv, int dtype, int64_t row_stride, const vo
  * head, query-tile pair) units cut into equal ranges, planned on the device;
  * repeated calls give identical bits.  total_tokens = 0 does nothing.
  * Workspace: jt_workspace_size(JT_OP_CHUNK_ATTN, nseq, 0, 0, 0, total_tokens,
- * Hq, Hkv, D, max_pages, max_chunk), sized for the current device; its first
- * 4096 bytes must be zero before its first use, and stay valid from call to
- * call.  A workspace of this operator serves calls of this operator only.
+ * Hq, Hkv, D, max_pages, max_chunk), sized for the current device (about 20 MB at
+ * D = 128 for bf16, up to 81 MB for fp32): a workspace for a program's most
+ * sequences, longest table and longest chunk serves all its calls, single tokens
+ * included.  bf16 calls need the size for max_pages = 1 only, whatever max_pages
+ * they have.  Its first 4096 bytes must be zero before its first use, and stay
+ * valid from call to call.  A workspace of this operator serves calls of this
+ * operator only.
  */
 jt_status jt_chunk_attn_paged(const void* q, const void* k_cache, const void* v_cache, int dtype,
                               const int32_t* block_table, int max_pages, int num_pages,

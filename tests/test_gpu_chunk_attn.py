@@ -394,3 +394,25 @@ def test_a_page_outside_the_pool_is_reported(dtype, D):
             assert bool(((out.double() - ref).abs()[keep] <= e_out[keep]).all())
     s["table"] = table
     check(s, *run(s, ws))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_a_workspace_for_prompts_serves_the_tokens_after_them(dtype):
+    prompt = batch(42, [0] * 12, [300 - 7 * i for i in range(12)], 8, 2, 64, dtype, max_pages=128)
+    ws = workspace(prompt)
+    check(prompt, *run(prompt, ws))
+    for n in (12, 3, 1):
+        s = batch(43 + n, [1900] * n, [1] * n, 8, 2, 64, dtype, max_pages=128)
+        check(s, *run(s, ws))
+
+
+def test_a_call_without_a_workspace_takes_what_its_type_needs():
+    s = batch(47, [4000] * 4, [1] * 4, 32, 8, 128)
+    run(s)
+    args = (s["q"], s["k"], s["v"], s["table"], s["L"], s["off"])
+    torch.cuda.synchronize()
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.memory_allocated()
+    out, lse = jt.jt_chunk_attn_paged(*args, max_chunk=1)
+    assert torch.cuda.max_memory_allocated() - before < 32 << 20
+    check(s, out, lse)

@@ -172,3 +172,37 @@ def test_rope_table():
         for j in range(8):
             a = pos * 1e4 ** (-2 * j / 16)
             assert abs(t[pos, j].item() - math.cos(a)) <= 2 ** -24 and abs(t[pos, 8 + j].item() - math.sin(a)) <= 2 ** -24
+
+
+SIZES = [(Hq, Hkv, D) for Hq, Hkv in ((32, 8), (8, 2), (64, 1), (128, 1), (6, 6)) for D in (32, 64, 96, 128)]
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", SIZES)
+def test_chunk_workspace_size_does_not_fall_when_sizes_grow(Hq, Hkv, D):
+    def size(nseq, pages, chunk):
+        return jt.jt_workspace_size(jt.JT_OP_CHUNK_ATTN, nseq, 0, 0, 0, nseq * chunk, Hq, Hkv, D, pages, chunk)
+
+    seqs, tables, chunks = (1, 2, 3, 7, 32, 100, 1000, 65535), (1, 2, 31, 32, 64, 512, 1 << 20), (1, 2, 16, 65, 512, 8192)
+    for n, n2 in zip(seqs, seqs[1:] + seqs[-1:]):
+        for p, p2 in zip(tables, tables[1:] + tables[-1:]):
+            for c, c2 in zip(chunks, chunks[1:] + chunks[-1:]):
+                at = size(n, p, c)
+                assert at <= size(n2, p, c) and at <= size(n, p2, c) and at <= size(n, p, c2), (n, p, c)
+
+
+@pytest.mark.parametrize("dtype", [0, 1])
+def test_a_chunk_workspace_serves_smaller_calls(dtype):
+    """A workspace for the most sequences, pages and tokens is accepted by every
+    smaller call (an output over its queries is refused after the workspace has been
+    accepted, so nothing is enqueued)."""
+    for nseq, pages, chunk in ((32, 512, 512), (8, 64, 8192), (300, 2048, 33)):
+        have = jt.jt_workspace_size(jt.JT_OP_CHUNK_ATTN, nseq, 0, 0, 0, 99, 32, 8, 128, pages, chunk)
+        for n in (1, 2, nseq // 2, nseq):
+            for p in (1, 32, pages):
+                for c in (1, 5, chunk):
+                    got = call("jt_chunk_attn_paged", CHUNK, dtype=dtype, nseq=n, max_pages=p, max_chunk=c, out=A, ws=W,
+                               ws_bytes=have)
+                    assert got == INVALID, (n, p, c)
+    if dtype == 1:  # bf16 needs the size for one page
+        small = jt.jt_workspace_size(jt.JT_OP_CHUNK_ATTN, 4, 0, 0, 0, 4, 32, 8, 128, 1, 1)
+        assert call("jt_chunk_attn_paged", CHUNK, nseq=4, max_pages=512, max_chunk=1, out=A, ws=W, ws_bytes=small) == INVALID

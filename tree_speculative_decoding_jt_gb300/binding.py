@@ -731,8 +731,10 @@ def jt_chunk_attn_paged(q, k_cache, v_cache, block_table, prefix_len, chunk_off,
         lse = torch.empty((total, Hq), dtype=torch.float32, device=q.device)
     if ws is None:
         with torch.cuda.device(idx):  # sized for the tensors' device
-            ws = workspace(jt_workspace_size(JT_OP_CHUNK_ATTN, nseq, 0, 0, 0, total, Hq, Hkv, D, max_pages, max_chunk),
-                           q.device)
+            ws = torch.empty(jt_workspace_size(JT_OP_CHUNK_ATTN, nseq, 0, 0, 0, total, Hq, Hkv, D,
+                                               1 if dtype == JT_DTYPE_BF16 else max_pages, max_chunk),
+                             dtype=torch.uint8, device=q.device)
+            ws[:4096].zero_()  # the part that must be zero
     rc = _packed(JT_OP_CHUNK_ATTN, idx, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), dtype,
                  block_table.data_ptr(), max_pages, num_pages, prefix_len.data_ptr(), chunk_off.data_ptr(), nseq,
                  total, max_chunk, Hq, Hkv, D, page, scale, out.data_ptr(), 0 if lse is None else lse.data_ptr(),

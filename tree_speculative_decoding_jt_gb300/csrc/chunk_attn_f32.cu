@@ -320,14 +320,17 @@ struct Plan {
 // batch's longest unit sets the time: 4 sequences of 16 to 512 tokens over 128 to
 // 1500 (8/2 heads, D 64) took 204 us with splits for less than one round only, and
 // take 86 (21 TFLOP/s of the visible pairs).
+static long long rounds() { return 16ll * std::max(1, device_sm_count()); }
+static long long max_splits(int max_pages) {
+    const long long tmax = (static_cast<long long>(max_pages) * JT_PAGE_SIZE + kKeys - 1) / kKeys;
+    return std::min(tmax / 4, static_cast<long long>(kMaxSplits));
+}
 static Plan plan(int nseq, int Hq, int Hkv, int max_pages, int max_chunk) {
     Plan pl;
     pl.npt = std::max(1, kRows / (Hq / Hkv));
     pl.mtiles = (max_chunk - 1) / pl.npt + 1;  // max_chunk may be INT_MAX
     pl.units = static_cast<long long>(nseq) * Hkv * pl.mtiles;
-    const long long tmax = (static_cast<long long>(max_pages) * JT_PAGE_SIZE + kKeys - 1) / kKeys;
-    const long long want = 16ll * std::max(1, device_sm_count()) / std::max(1ll, pl.units);
-    pl.splits = static_cast<int>(std::max(1ll, std::min({want, tmax / 4, static_cast<long long>(kMaxSplits)})));
+    pl.splits = static_cast<int>(std::max(1ll, std::min(rounds() / std::max(1ll, pl.units), max_splits(max_pages))));
     return pl;
 }
 
@@ -376,11 +379,24 @@ static cudaError_t launch(const ChunkArgs& a, char* ws, cudaStream_t st) {
 
 }  // namespace chunk32
 
-size_t chunk_attn_f32_workspace_bytes(int nseq, int Hq, int Hkv, int D, int max_pages, int max_chunk) {
-    const chunk32::Plan pl = chunk32::plan(nseq, Hq, Hkv, max_pages, max_chunk);
-    if (pl.splits == 1) return kChunkFixedBytes;
-    const size_t rows = static_cast<size_t>(pl.units) * pl.splits * chunk32::kRows;
+static size_t f32_bytes(long long splits, int D) {  // partial results of `splits` (unit, split) tiles
+    const size_t rows = static_cast<size_t>(splits) * chunk32::kRows;
     return kChunkFixedBytes + align_up(rows * sizeof(float2)) + align_up(rows * D * sizeof(float));
+}
+
+size_t chunk_attn_f32_need_bytes(int nseq, int Hq, int Hkv, int D, int max_pages, int max_chunk) {
+    const chunk32::Plan pl = chunk32::plan(nseq, Hq, Hkv, max_pages, max_chunk);
+    return pl.splits == 1 ? kChunkFixedBytes : f32_bytes(pl.units * pl.splits, D);
+}
+
+// A call with fewer units splits them further, so its need can be the larger one.
+// What is reported covers every call with at most these sequences, pages and
+// chunk lengths: units * splits is at most rounds() and at most units * max_splits.
+size_t chunk_attn_f32_workspace_bytes(int nseq, int Hq, int Hkv, int D, int max_pages, int max_chunk) {
+    const long long per = chunk32::max_splits(max_pages);
+    if (per < 2) return kChunkFixedBytes;
+    const long long units = std::min(chunk32::plan(nseq, Hq, Hkv, max_pages, max_chunk).units, chunk32::rounds());
+    return f32_bytes(std::min(units * per, chunk32::rounds()), D);
 }
 
 cudaError_t chunk_attn_f32_launch(const ChunkArgs& a, char* ws, cudaStream_t st) {

@@ -392,7 +392,7 @@ jt_status jt_chunk_attn_paged(const void* q, const void* k_cache, const void* v_
         return JT_ERR_INVALID;
     jt_status s = check_ws(ws, ws_bytes,
                            bf16 ? chunk_attn_bf16_workspace_bytes(D)
-                                : chunk_attn_f32_workspace_bytes(nseq, Hq, Hkv, D, max_pages, max_chunk));
+                                : chunk_attn_f32_need_bytes(nseq, Hq, Hkv, D, max_pages, max_chunk));
     if (s != JT_OK) return s;
     const int64_t bytes = static_cast<int64_t>(total_tokens) * Hq * D * (bf16 ? 2 : 4);
     if (overlap(q, bytes, out, bytes)) return JT_ERR_INVALID;  // other CTAs may still read the queries of a row written

@@ -120,8 +120,10 @@ struct ChunkArgs {
 };
 // header and merge counts: zero before a workspace's first use
 constexpr size_t kChunkFixedBytes = 4096;
-// whole workspace (header included) of a call on the current device
+// whole workspace (header included) on the current device: bf16, fp32 (of a call;
+// of any call up to these sizes)
 size_t chunk_attn_bf16_workspace_bytes(int D);
+size_t chunk_attn_f32_need_bytes(int nseq, int Hq, int Hkv, int D, int max_pages, int max_chunk);
 size_t chunk_attn_f32_workspace_bytes(int nseq, int Hq, int Hkv, int D, int max_pages, int max_chunk);
 cudaError_t chunk_attn_bf16_launch(const ChunkArgs& a, char* ws, cudaStream_t st);
 cudaError_t chunk_attn_f32_launch(const ChunkArgs& a, char* ws, cudaStream_t st);
