@@ -526,7 +526,8 @@ jt_status jt_chunk_attn_paged(const void* q, const void* k_cache, const void* v_
  *             (JT_ERR_INVALID).
  *   accept_len, path (int32 [nseq], [nseq, N+1]): jt_verify_accept*'s outputs.
  *   prefix_len, tree_off, block_table: as in jt_tree_attn_paged.
- *   new_prefix: int32 [nseq]; may be prefix_len itself (updated in place).
+ *   new_prefix: int32 [nseq]; may be prefix_len itself (updated in place), else
+ *             it overlaps none of the other arrays (JT_ERR_INVALID).
  * A sequence whose accept_len, path (strictly rising from node 0), lengths or
  * pages are out of range keeps its cache, its new_prefix entry is left as it
  * was, and JT_ERR_INVALID is raised (device-side).  Pages that hold slots L_b ..

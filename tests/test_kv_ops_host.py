@@ -206,3 +206,18 @@ def test_a_chunk_workspace_serves_smaller_calls(dtype):
     if dtype == 1:  # bf16 needs the size for one page
         small = jt.jt_workspace_size(jt.JT_OP_CHUNK_ATTN, 4, 0, 0, 0, 4, 32, 8, 128, 1, 1)
         assert call("jt_chunk_attn_paged", CHUNK, nseq=4, max_pages=512, max_chunk=1, out=A, ws=W, ws_bytes=small) == INVALID
+
+
+def far(**at):
+    """COMMIT's arrays, each far from the others, and a workspace that is enough."""
+    names = ("k_cache", "v_cache", "block_table", "prefix_len", "tree_off", "accept_len", "path", "new_prefix")
+    apart = {n: ctypes.c_void_p((i + 1) << 32) for i, n in enumerate(names)}
+    return dict(apart, ws=W, ws_bytes=1 << 20, **{n: ctypes.c_void_p(apart[m].value + shift) for n, (m, shift) in at.items()})
+
+
+@pytest.mark.parametrize("name,size", [("prefix_len", 8), ("accept_len", 8), ("tree_off", 12), ("path", 2 * 9 * 4),
+                                       ("block_table", 2 * 4 * 4)])
+def test_commit_refuses_new_lengths_over_what_it_reads(name, size):
+    """The CTAs of one cache write the new lengths while those of the others may still read."""
+    for shift in (-4, 4, size - 4) + ((0,) if name != "prefix_len" else ()):
+        assert call("jt_kv_commit", COMMIT, **far(new_prefix=(name, shift))) == INVALID, shift

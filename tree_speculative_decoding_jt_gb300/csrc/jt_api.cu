@@ -442,6 +442,10 @@ jt_status jt_kv_commit(void* k_cache, void* v_cache, int dtype, int layers, int6
     if (!in_place && overlap(new_prefix, n, prefix_len, n)) return JT_ERR_INVALID;
     jt_status s = check_ws(ws, ws_bytes, in_place ? kv_commit_workspace_bytes(nseq) : kWsHeader);
     if (s != JT_OK) return s;
+    // CTAs write new_prefix while others still read these (in place, all of them have been read by then)
+    if (!in_place && (overlap(new_prefix, n, accept_len, n) || overlap(new_prefix, n, tree_off, n + 4) ||
+                      overlap(new_prefix, n, path, n * (N + 1)) || overlap(new_prefix, n, block_table, n * max_pages)))
+        return JT_ERR_INVALID;
     if (k_cache == v_cache) return JT_ERR_INVALID;  // two CTAs would move the same path
     CommitArgs a;
     a.k_cache = k_cache;
