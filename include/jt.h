@@ -522,12 +522,13 @@ jt_status jt_chunk_attn_paged(const void* q, const void* k_cache, const void* v_
  *   k_cache, v_cache: `layers` caches [num_pages, page_size, Hkv, D] (dtype),
  *             layer_stride elements apart (one layer: any value); the block
  *             table serves all layers.  Hkv * D * element size is a multiple
- *             of 16, else JT_ERR_UNSUPPORTED.  k_cache is not v_cache
- *             (JT_ERR_INVALID).
+ *             of 16, else JT_ERR_UNSUPPORTED.  No layer of k_cache meets one of
+ *             v_cache (JT_ERR_INVALID); the layers of the two may alternate.
  *   accept_len, path (int32 [nseq], [nseq, N+1]): jt_verify_accept*'s outputs.
  *   prefix_len, tree_off, block_table: as in jt_tree_attn_paged.
  *   new_prefix: int32 [nseq]; may be prefix_len itself (updated in place), else
- *             it overlaps none of the other arrays (JT_ERR_INVALID).
+ *             it overlaps none of prefix_len, tree_off, accept_len, path and
+ *             block_table (JT_ERR_INVALID).
  * A sequence whose accept_len, path (strictly rising from node 0), lengths or
  * pages are out of range keeps its cache, its new_prefix entry is left as it
  * was, and JT_ERR_INVALID is raised (device-side).  Pages that hold slots L_b ..

@@ -208,6 +208,9 @@ def test_a_chunk_workspace_serves_smaller_calls(dtype):
         assert call("jt_chunk_attn_paged", CHUNK, nseq=4, max_pages=512, max_chunk=1, out=A, ws=W, ws_bytes=small) == INVALID
 
 
+POOL = 9 * 16 * 8 * 128 * 2  # bytes of one layer of COMMIT
+
+
 def far(**at):
     """COMMIT's arrays, each far from the others, and a workspace that is enough."""
     names = ("k_cache", "v_cache", "block_table", "prefix_len", "tree_off", "accept_len", "path", "new_prefix")
@@ -221,3 +224,15 @@ def test_commit_refuses_new_lengths_over_what_it_reads(name, size):
     """The CTAs of one cache write the new lengths while those of the others may still read."""
     for shift in (-4, 4, size - 4) + ((0,) if name != "prefix_len" else ()):
         assert call("jt_kv_commit", COMMIT, **far(new_prefix=(name, shift))) == INVALID, shift
+
+
+@pytest.mark.parametrize("layers,stride,shift", [
+    (1, POOL, 0), (1, POOL, 16), (1, POOL, POOL - 16), (1, POOL, 16 - POOL),
+    (2, POOL, POOL), (2, POOL, -POOL), (2, POOL, 2 * POOL - 16), (2, 2 * POOL, POOL + 16), (2, 2 * POOL, 16 - POOL),
+    (36, 2 * POOL, 35 * 2 * POOL), (36, 2 * POOL, 34 * 2 * POOL + POOL - 16), (36, 2 * POOL, -35 * 2 * POOL - 16),
+    (36, 3 * POOL + 64, 7 * (3 * POOL + 64) + POOL - 16),
+])
+def test_commit_refuses_layers_of_keys_that_meet_layers_of_values(layers, stride, shift):
+    """Two CTAs would move the same rows."""
+    assert call("jt_kv_commit", COMMIT, **far(v_cache=("k_cache", shift)), layers=layers,
+                layer_stride=stride // 2) == INVALID

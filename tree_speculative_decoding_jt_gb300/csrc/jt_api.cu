@@ -37,6 +37,17 @@ static bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
     return na > 0 && nb > 0 && x < y + static_cast<uintptr_t>(nb) && y < x + static_cast<uintptr_t>(na);
 }
 
+// Whether some layer of k meets some layer of v: `layers` pools of n bytes each,
+// stride >= n bytes apart.
+static bool layers_meet(const void* k, const void* v, int64_t n, int64_t stride, int layers) {
+    const int64_t d = static_cast<int64_t>(reinterpret_cast<uintptr_t>(v) - reinterpret_cast<uintptr_t>(k));
+    if (layers == 1) return d > -n && d < n;
+    // layers t apart differ by d + t * stride: the nearest to 0 are beside t = -d / stride
+    for (int64_t t = -d / stride - 1; t <= -d / stride + 1; ++t)
+        if (t > -layers && t < layers && d + t * stride > -n && d + t * stride < n) return true;
+    return false;
+}
+
 static jt_status check_ws(void* ws, size_t ws_bytes, size_t need) {
     if (!ws || !aligned(ws, kAlign) || ws_bytes < need) return JT_ERR_WORKSPACE;
     return JT_OK;
@@ -446,7 +457,10 @@ jt_status jt_kv_commit(void* k_cache, void* v_cache, int dtype, int layers, int6
     if (!in_place && (overlap(new_prefix, n, accept_len, n) || overlap(new_prefix, n, tree_off, n + 4) ||
                       overlap(new_prefix, n, path, n * (N + 1)) || overlap(new_prefix, n, block_table, n * max_pages)))
         return JT_ERR_INVALID;
-    if (k_cache == v_cache) return JT_ERR_INVALID;  // two CTAs would move the same path
+    // two CTAs would move the same path
+    if (layers_meet(k_cache, v_cache, static_cast<int64_t>(num_pages) * JT_PAGE_SIZE * row,
+                    layers > 1 ? layer_stride * esize : 0, layers))
+        return JT_ERR_INVALID;
     CommitArgs a;
     a.k_cache = k_cache;
     a.v_cache = v_cache;
