@@ -342,3 +342,51 @@ def test_commit_leaves_bad_sequences_alone(in_place):
         assert e.value.status == jt.JT_ERR_INVALID, (name, at, val)
         assert out.tolist() == [int(n[0]), before, int(n[2])], (name, at, val)
         assert torch.equal(bits(s["k"]), bits(k)) and torch.equal(bits(s["v"]), bits(v)), (name, at, val)
+
+
+@pytest.mark.parametrize("layout", ["alternating", "apart", "split"])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_commit_in_pools_whose_layers_lie_apart(layout, in_place):
+    """Keys and values of a layer side by side in one pool, layers with other
+    tensors between them, and the halves of one pool: what lies between stays."""
+    s = commit_case(230, [100, 0, 15], [64, 17, 40], [8, 0, 3], 8, 4, 64, BF16, 5)
+    k, v, n = commit_ref(s)
+    shape = s["k"].shape
+    if layout == "alternating":
+        pool = torch.zeros((5, 2) + shape[1:], dtype=BF16, device="cuda")
+        kc, vc = pool[:, 0], pool[:, 1]
+    elif layout == "apart":
+        pool = torch.zeros((5, 3) + shape[1:], dtype=BF16, device="cuda")
+        kc, vc = pool[:, 2], pool[:, 0]
+    else:
+        pool = torch.zeros((2,) + shape, dtype=BF16, device="cuda")
+        kc, vc = pool[1], pool[0]
+    kc.copy_(s["k"])
+    vc.copy_(s["v"])
+    ws = jt.workspace(jt.jt_workspace_size(jt.JT_OP_KV_COMMIT, 3))
+    out = jt.jt_kv_commit(kc, vc, s["table"], s["L"], s["off"], s["accept"], s["path"],
+                          new_prefix=s["L"] if in_place else None, ws=ws)
+    jt.jt_check(ws)
+    assert torch.equal(bits(kc.contiguous()), bits(k)) and torch.equal(bits(vc.contiguous()), bits(v))
+    assert torch.equal(out, n)
+    if layout == "apart":
+        assert not bool(pool[:, 1].any())
+
+
+def test_commit_refuses_layers_that_it_cannot_step_through():
+    s = commit_case(231, [10], [8], [2], 4, 4, 64, BF16, 4)
+    rest = (s["table"], s["L"], s["off"], s["accept"], s["path"])
+    shape = s["k"].shape
+    wide = torch.zeros((4, 2) + shape[1:], dtype=BF16, device="cuda")
+    heads = torch.zeros(shape[:3] + (8, 64), dtype=BF16, device="cuda")
+    with pytest.raises(ValueError, match="distances apart"):
+        jt.jt_kv_commit(s["k"], wide[:, 0], *rest)
+    for k, v in ((heads[:, :, :, :4], heads[:, :, :, 4:]), (s["k"], heads[:, :, :, :4])):
+        with pytest.raises(ValueError):
+            jt.jt_kv_commit(k, v, *rest)
+    with pytest.raises(ValueError):
+        jt.jt_kv_commit(s["k"], s["v"][:3], *rest)
+    with pytest.raises(jt.JtError):  # layers that overlap
+        jt.jt_kv_commit(wide[0, 0].expand(4, *shape[1:]), wide[0, 1].expand(4, *shape[1:]), *rest)
+    with pytest.raises(jt.JtError):  # the same pool twice
+        jt.jt_kv_commit(wide[:, 0], wide[:, 0], *rest)

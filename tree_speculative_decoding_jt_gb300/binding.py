@@ -577,6 +577,16 @@ def _like(t, name, dtype, idx, shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
+def _layers(t, name, dtype, idx, shape):
+    """Check a cache whose layers (the first of five dimensions) are contiguous,
+    but may lie apart; the elements from one to the next."""
+    if len(shape) == 5 and isinstance(t, torch.Tensor) and t.shape == shape and not t.is_contiguous():
+        _like(t[0], name, dtype, idx, shape[1:])
+        return t.stride(0)
+    _like(t, name, dtype, idx, shape)
+    return shape[-4] * shape[-3] * shape[-2] * shape[-1]
+
+
 def _tables(block_table, prefix_len, off, off_name, idx):
     """(nseq, max_pages) of a batch's checked tables."""
     if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
@@ -750,15 +760,18 @@ def jt_kv_commit(k_cache, v_cache, block_table, prefix_len, tree_off, accept_len
     the prefix lengths.
 
     k/v_cache [pages, 16, Hkv, D] or [layers, pages, 16, Hkv, D] (bf16 or fp32,
-    updated in place); accept_len [nseq], path [nseq, N+1] int32 as
+    updated in place; the layers contiguous, and the same distance apart in both:
+    kv[:, 0] and kv[:, 1] of a [layers, 2, pages, 16, Hkv, D] pool do); accept_len [nseq], path [nseq, N+1] int32 as
     jt_verify_accept returns them; new_prefix: int32 [nseq] output, prefix_len
     itself to update it in place, None for a new tensor.  Returns new_prefix."""
     idx, dtype = _lead(k_cache, "k_cache")
     kv_shape = k_cache.shape
     if len(kv_shape) not in (4, 5):
         raise ValueError("k_cache must be [pages, 16, Hkv, D] or [layers, pages, 16, Hkv, D]")
-    _like(k_cache, "k_cache", k_cache.dtype, idx, kv_shape)
-    _like(v_cache, "v_cache", k_cache.dtype, idx, kv_shape)
+    layers = kv_shape[0] if len(kv_shape) == 5 else 1
+    layer_stride = _layers(k_cache, "k_cache", k_cache.dtype, idx, kv_shape)
+    if _layers(v_cache, "v_cache", k_cache.dtype, idx, kv_shape) != layer_stride:
+        raise ValueError("the layers of k_cache and v_cache are different distances apart")
     nseq, max_pages = _tables(block_table, prefix_len, tree_off, "tree_off", idx)
     _like(accept_len, "accept_len", torch.int32, idx, (nseq,))
     if not isinstance(path, torch.Tensor) or path.dim() != 2:
@@ -766,7 +779,6 @@ def jt_kv_commit(k_cache, v_cache, block_table, prefix_len, tree_off, accept_len
     width = path.shape[1]
     _like(path, "path", torch.int32, idx, (nseq, width))
     num_pages, page, Hkv, D = kv_shape[-4:]
-    layers = kv_shape[0] if len(kv_shape) == 5 else 1
     if new_prefix is None:
         new_prefix = torch.empty_like(prefix_len)
     elif new_prefix is not prefix_len:
@@ -774,7 +786,7 @@ def jt_kv_commit(k_cache, v_cache, block_table, prefix_len, tree_off, accept_len
     if ws is None:
         ws = workspace(jt_workspace_size(JT_OP_KV_COMMIT, nseq), k_cache.device)
     rc = _packed(JT_OP_KV_COMMIT, idx, k_cache.data_ptr(), v_cache.data_ptr(), dtype, layers,
-                 num_pages * page * Hkv * D, block_table.data_ptr(), max_pages, num_pages, prefix_len.data_ptr(),
+                 layer_stride, block_table.data_ptr(), max_pages, num_pages, prefix_len.data_ptr(),
                  tree_off.data_ptr(), accept_len.data_ptr(), path.data_ptr(), nseq, width - 1, Hkv, D, page,
                  new_prefix.data_ptr(), ws.data_ptr(), _workspace_of(ws, idx))
     if rc != JT_OK:
