@@ -484,8 +484,8 @@ jt_status jt_qkv_append(const void* qkv, int dtype, int64_t row_stride, const vo
  *             fp32: D in {32, 64, 96, 128}, Hq/Hkv <= 64; else
  *             JT_ERR_UNSUPPORTED.  scale > 0.
  *   out:      [total_tokens, Hq, D] (dtype), lse: fp32 [total_tokens, Hq] or
- *             NULL, as in jt_tree_attn_paged.  out does not overlap q
- *             (JT_ERR_INVALID).
+ *             NULL, as in jt_tree_attn_paged.  out and lse overlap neither q, the
+ *             caches nor each other (JT_ERR_INVALID).
  * A page outside the pool among those a sequence's tokens see raises
  * JT_ERR_INVALID (device-side); its keys and values are taken as zeros, so what
  * the sequence's rows hold then says nothing.  Other sequences are not touched.

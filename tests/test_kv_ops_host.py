@@ -236,3 +236,16 @@ def test_commit_refuses_layers_of_keys_that_meet_layers_of_values(layers, stride
     """Two CTAs would move the same rows."""
     assert call("jt_kv_commit", COMMIT, **far(v_cache=("k_cache", shift)), layers=layers,
                 layer_stride=stride // 2) == INVALID
+
+
+@pytest.mark.parametrize("dtype", [0, 1])
+@pytest.mark.parametrize("a,b", [("out", "q"), ("out", "k_cache"), ("out", "v_cache"), ("lse", "q"), ("lse", "out"),
+                                 ("lse", "k_cache"), ("lse", "v_cache")])
+def test_chunk_refuses_outputs_over_what_it_reads(a, b, dtype):
+    apart = {n: ctypes.c_void_p((i + 1) << 32) for i, n in enumerate(("q", "k_cache", "v_cache", "out", "lse"))}
+    esize = 2 if dtype else 4
+    size = dict(q=5 * 32 * 128 * esize, out=5 * 32 * 128 * esize, lse=5 * 32 * 4)
+    size["k_cache"] = size["v_cache"] = 9 * 16 * 8 * 128 * esize
+    for shift in (0, 16, 16 - size[a], size[b] - 16):
+        apart[a] = ctypes.c_void_p(apart[b].value + shift)
+        assert call("jt_chunk_attn_paged", CHUNK, **apart, dtype=dtype, ws=W, ws_bytes=1 << 34) == INVALID, shift

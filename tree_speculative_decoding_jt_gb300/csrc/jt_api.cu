@@ -406,7 +406,13 @@ jt_status jt_chunk_attn_paged(const void* q, const void* k_cache, const void* v_
                                 : chunk_attn_f32_need_bytes(nseq, Hq, Hkv, D, max_pages, max_chunk));
     if (s != JT_OK) return s;
     const int64_t bytes = static_cast<int64_t>(total_tokens) * Hq * D * (bf16 ? 2 : 4);
-    if (overlap(q, bytes, out, bytes)) return JT_ERR_INVALID;  // other CTAs may still read the queries of a row written
+    // other CTAs may still read the queries, keys and values of a row written
+    const int64_t pool = static_cast<int64_t>(num_pages) * JT_PAGE_SIZE * Hkv * D * (bf16 ? 2 : 4);
+    const int64_t rows = lse ? static_cast<int64_t>(total_tokens) * Hq * 4 : 0;
+    if (overlap(q, bytes, out, bytes) || overlap(out, bytes, k_cache, pool) || overlap(out, bytes, v_cache, pool) ||
+        overlap(lse, rows, q, bytes) || overlap(lse, rows, out, bytes) || overlap(lse, rows, k_cache, pool) ||
+        overlap(lse, rows, v_cache, pool))
+        return JT_ERR_INVALID;
     ChunkArgs a;
     a.q = q;
     a.k_cache = k_cache;
