@@ -484,7 +484,11 @@ jt_status jt_qkv_append(const void* qkv, int dtype, int64_t row_stride, const vo
  *             fp32: D in {32, 64, 96, 128}, Hq/Hkv <= 64; else
  *             JT_ERR_UNSUPPORTED.  scale > 0.
  *   out:      [total_tokens, Hq, D] (dtype), lse: fp32 [total_tokens, Hq] or
- *             NULL, as in jt_tree_attn_paged.  out and lse overlap neither q, the
+ *             NULL, as in jt_tree_attn_paged.  Scores, maxima, sums and out's
+ *             accumulation are fp32.  bf16: each probability is rounded to bf16
+ *             (at most 2^-8 of it) for the product with the values, their sum
+ *             (and so lse) is of the unrounded ones, and out is rounded once;
+ *             fp32: nothing is rounded below fp32.  out and lse overlap neither q, the
  *             caches nor each other (JT_ERR_INVALID).
  * A page outside the pool among those a sequence's tokens see raises
  * JT_ERR_INVALID (device-side); its keys and values are taken as zeros, so what

@@ -416,3 +416,38 @@ def test_a_call_without_a_workspace_takes_what_its_type_needs():
     out, lse = jt.jt_chunk_attn_paged(*args, max_chunk=1)
     assert torch.cuda.max_memory_allocated() - before < 32 << 20
     check(s, out, lse)
+
+
+@pytest.mark.parametrize("D", [128, 64])
+def test_a_probability_is_rounded_once_when_the_maximum_jumps(D):
+    """Scores of 0 in the first key tile, 40 to 48 (log2 units) for a key of the
+    second, 0 to 24 for a key of the third: the third tile's P is worked out before
+    its warp knows of the jump and scaled afterwards.  Only that key has a value, so a
+    row's error is P's rounding and the output's: two half steps of 2^-8 (and 2^-15
+    for the fp32 terms: some 50 half steps of 2^-24 in the score, 2^-22 in exp2)."""
+    nseq, L, B, Hq, Hkv = 40, 384, 32, 16, 4
+    s = batch(60, [L] * nseq, [B] * nseq, Hq, Hkv, D)
+    unit = math.log2(math.e) / math.sqrt(D)  # of a score in log2 units
+    g = torch.Generator(device="cuda")
+    g.manual_seed(61)
+
+    def rand(*shape):
+        return torch.rand(shape, generator=g, device="cuda")
+
+    q = torch.zeros_like(s["q"])
+    q[..., 0] = (1 + 0.2 * rand(*q.shape[:2])).to(BF16)
+    q[..., 1] = (24 * rand(*q.shape[:2])).to(BF16)
+    s["q"] = q
+    k, v = torch.zeros_like(s["k"]), torch.zeros_like(s["v"])
+    for b in range(nseq):
+        page, row = slots(s["table"], b, 128 + 5, 1)
+        k[page, row, :, 0] = 40 / unit
+        page, row = slots(s["table"], b, 256 + 7, 1)
+        k[page, row, :, 1] = 1 / unit
+        v[page, row] = ((1 + rand(Hkv, D)) * 2.0 ** 40).to(BF16)
+    s["k"], s["v"] = k, v
+    out, lse = run(s)
+    ref, rlse, _, _ = chunk_ref(s)
+    half = 2.0 ** -8
+    assert bool(((out.double() - ref).abs() <= ref * ((1 + half) ** 2 * (1 + 2.0 ** -15) - 1)).all())
+    assert bool(((lse.double() - rlse).abs() <= 2.0 ** -16).all())

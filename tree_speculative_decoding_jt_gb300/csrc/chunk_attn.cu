@@ -6,8 +6,10 @@
 // the slots 0 .. L_b + i:
 //     out = sum_s exp(scale q.k_s - m) v_s / l,  l = sum_s exp(scale q.k_s - m),
 // one pass over the keys with the running maximum m and sum l (fp32), P =
-// exp(...) rounded to bf16 for the second product (at most 2^-8 relative, as the
-// inputs are; l sums the unrounded values), the output rounded once.
+// exp(...) rounded once to bf16 for the second product (at most 2^-8 relative, as
+// the inputs are; l sums the unrounded values), the output rounded once.  The
+// product takes operands of one type, so P held finer would mean V in two parts and
+// twice the MMAs; a prompt is bound by the chain that they are part of.
 //
 // Work.  A unit is (sequence b, KV head g, query-tile pair mp): two 128-row
 // query tiles of npt = 128 / G new tokens x the G query heads of KV head g
@@ -29,10 +31,11 @@
 //              has two tiles' time for one tile's softmax.  P of all tiles of a
 //              row is relative to one maximum m: each warp keeps the m it knows
 //              and its own part of the sum, and tells the other m after every
-//              tile.  m is the first tile's maximum, raised only when a later
-//              score exceeds it by 2^32: P, O and l then stay far inside fp32,
-//              with no loss of relative precision, and the partner's m is not on
-//              the way of a tile's exponentials.  Warps whose rows are all past
+//              tile.  m is the first tile's maximum, rounded up to a whole number
+//              of log2 units and raised only when a later score exceeds it by
+//              2^32: P, O and l then stay far inside fp32, with no loss of relative
+//              precision, a change of m scales by powers of two, and the partner's
+//              m is not on the way of a tile's exponentials.  Warps whose rows are all past
 //              the chunk's end (single tokens fill 1 to 16 of 256 rows) compute
 //              nothing.
 //   8-11       epilogue: O of a piece to the output or to its partial, and the
@@ -1241,7 +1244,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         }
                         if (j == 1) m_run = m_o;
                     }
-                    if (mx_s > m_run + kRescaleLog2 || m_run == -INFINITY) m_run = fmaxf(m_run, mx_s);
+                    // a whole number of log2 units: a change of m then scales P and O
+                    // by a power of two, and P is rounded once whatever m was then
+                    if (mx_s > m_run + kRescaleLog2 || m_run == -INFINITY) m_run = ceilf(fmaxf(m_run, mx_s));
                     if (j == 0) tell_partner(t, m_run);  // early: the partner's first tile waits for it
                     // P = exp2(s*scale*log2e - m), written over S (bf16 pairs)
                     float sum = row_exp(tS, sl2, m_run == -INFINITY ? 0.0f : m_run);
