@@ -51,14 +51,16 @@
 //
 // What bounds it, measured (32/8 heads, D 128 unless said; flops of the visible
 // (token, key) pairs, bytes read and written once):
-//   8192 tokens on 8192           1120-1160 us, 1.42-1.47 PFLOP/s: the chain score
+//   8192 tokens on 8192           1075-1155 us, 1.43-1.53 PFLOP/s: the chain score
 //     -> softmax -> P -> output MMA of a tile over three S buffers (1650 cycles a
 //     tile where its MMAs take 1080);
-//   16 sequences, 1 to 512 tokens on 1024 to 8192   199 us, 1.0 PFLOP/s: the same,
-//     0.11 of the work past the chunks' ends, and some 2.5 us a piece;
-//   32 single tokens on 32768     650 us, 6.6 TB/s: HBM;
-//   1 token on 4096               18.6 us: latency (plan, 3 or 4 tiles, merge);
-//   D 64, 5 chunks of up to 1500  106 us: exponentials and pieces.
+//   16 sequences, 1 to 512 tokens on 1024 to 8192   200-215 us, 0.92-1.0 PFLOP/s: the
+//     same, 0.11 of the work past the chunks' ends, and some 2.5 us a piece;
+//   32 single tokens on 32768     653-713 us, 6.0-6.6 TB/s: HBM;
+//   1 token on 4096               19.5 us from HBM, 18.4 from the L2: latency (plan, 3
+//     or 4 tiles, merge);
+//   D 64, 5 chunks of up to 1500  107 us: exponentials and pieces
+// (ranges: from GPU to GPU, and replayed back to back or call by call).
 // A tile's row maximum taken by the TMEM load itself, P released in halves, the
 // exponential as a polynomial, scores in halves of 64 keys, and the piece cut by a
 // range's end done first (its merge then amid the others) were slower or equal.

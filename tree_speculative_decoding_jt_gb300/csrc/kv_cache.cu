@@ -22,8 +22,9 @@ namespace kv {
 // with one token: its angles sit in registers for all heads, four heads' loads
 // are in flight per lane.  Bound: HBM bytes (one read, one write of every
 // element) for many tokens, a chain of dependent loads (offsets, prefix, page,
-// row) for one.  Measured (32/8 heads, D 128): 22610 tokens 98 us, 5.8 TB/s; 8
-// trees of 256 nodes 9.3 us, 5.5 TB/s; one token 2.3 us.
+// row) for one.  Measured (32/8 heads, D 128; data from HBM): 22610 tokens 100 us,
+// 5.7 TB/s; 8 trees of 256 nodes 13.4 us, 3.8 TB/s (9.7 us where the 51 MB are in
+// the L2 already); one token 2.3 us.
 // ---------------------------------------------------------------------------
 struct Append {
     const void* qkv;
@@ -279,7 +280,8 @@ static cudaError_t append_launch(Append prm, cudaStream_t st) {
     // and angles are looked up once, and its heads are read four per lane group
     // at a time (22610 tokens of 32/8 heads, D 128: 98 us with one warp a token,
     // 110 with two, 117 with three).  Few tokens get up to one lane group per
-    // head (761 tokens of 12/4 heads, D 96, fp32: 6.2 us with one, 4.7 with three).
+    // head (761 tokens of 12/4 heads, D 96, fp32, data in the L2: 6.2 us with one,
+    // 4.7 with three).
     const long long fine = (H + per - 1) / per;
     prm.warps_per_token = static_cast<int>(
         std::max(1ll, std::min(fine, (12ll * device_sm_count() + prm.total - 1) / prm.total)));
@@ -302,8 +304,8 @@ static cudaError_t append_launch(Append prm, cudaStream_t st) {
 // the row offsets of the whole path worked out once per CTA.  grid (nseq,
 // layer-halves): a CTA takes every gridDim.y-th of the 2 * layers caches.
 // Bound: HBM bytes of the moved rows; for one sequence the chain accept_len ->
-// path -> page -> row.  Measured (36 layers, 8 heads, D 128): 32 sequences 6.1 us,
-// 6.6 TB/s; one sequence 2.2 us.
+// path -> page -> row.  Measured (36 layers, 8 heads, D 128): 32 sequences, 40 MB,
+// 9.5 us from HBM, 4.2 TB/s (6.2 us where they are in the L2); one sequence 2.2 us.
 // ---------------------------------------------------------------------------
 struct Commit {
     char* k_cache;
